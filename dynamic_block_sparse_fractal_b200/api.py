@@ -7,6 +7,7 @@ library has not been built, every call raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Tuple
 
@@ -35,7 +36,9 @@ SYMBOLS = (
     "sparse_attn_bwd_scratch_size_heads", "sparse_attn_bwd_heads",
     "sparse_attn_block_heatmap_scratch_size_heads", "sparse_attn_block_heatmap_heads",
     "sparse_attn_plan_profile", "sparse_attn_plan_stage_name",
-    "sparse_attn_token_entropy", "sparse_attn_plan_radius",
+    "sparse_attn_token_entropy", "sparse_attn_plan_radius", "sparse_attn_plan_mask",
+    "sparse_attn_fwd_bias", "sparse_attn_bwd_bias_scratch_size", "sparse_attn_bwd_bias",
+    "sparse_attn_fwd_diff", "sparse_attn_bwd_diff_scratch_size", "sparse_attn_bwd_diff",
 )
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -58,6 +61,11 @@ class SaMaskViews(ctypes.Structure):
                 ("idx", ctypes.c_void_p), ("tile_cnt", ctypes.c_void_p),
                 ("tile_idx", ctypes.c_void_p), ("nb", ctypes.c_int), ("ntile", ctypes.c_int),
                 ("logits", ctypes.c_void_p), ("logits_ld", ctypes.c_int)]
+
+
+class SaRelBias(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("bucket", ctypes.c_void_p),
+                ("n_buckets", ctypes.c_int)]
 
 
 class SparseAttnError(RuntimeError):
@@ -99,6 +107,14 @@ def lib() -> ctypes.CDLL:
                                                ctypes.POINTER(ctypes.c_float), i32, ip, vp]
         L.sparse_attn_token_entropy.argtypes = [dp, vp, vp, vp, sz, vp, vp]
         L.sparse_attn_plan_radius.argtypes = [dp, ctypes.POINTER(SaRadius), vp, vp, sz, vp]
+        L.sparse_attn_plan_mask.argtypes = [dp, vp, i32, vp, sz, vp]
+        bp = ctypes.POINTER(SaRelBias)
+        L.sparse_attn_fwd_bias.argtypes = [dp, bp, vp, vp, vp, vp, sz, vp, vp, vp]
+        L.sparse_attn_bwd_bias.argtypes = [dp, bp] + [vp] * 7 + [sz] + [vp] * 5 + [sz, vp]
+        L.sparse_attn_fwd_diff.argtypes = [dp, vp, vp, vp, vp, vp, sz, vp, vp, vp, vp]
+        L.sparse_attn_bwd_diff.argtypes = [dp] + [vp] * 9 + [sz] + [vp] * 5 + [sz, vp]
+        L.sparse_attn_bwd_bias_scratch_size.argtypes = [dp, ctypes.POINTER(sz)]
+        L.sparse_attn_bwd_diff_scratch_size.argtypes = [dp, ctypes.POINTER(sz)]
         L.sparse_attn_status_string.argtypes = [i32]
         L.sparse_attn_status_string.restype = ctypes.c_char_p
         L.sparse_attn_plan_stage_name.argtypes = [i32]
@@ -362,6 +378,185 @@ def get_mask(desc: SaDesc, workspace: torch.Tensor) -> dict:
         "logits": view(v.logits, BH * nb * v.logits_ld, torch.float32,
                        (BH, nb, v.logits_ld))[:, :, :nb],
     }
+
+
+# ---- the caller's own mask, and other score functions over any plan ------------
+
+def plan_mask(desc: SaDesc, mask: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """Plan from a block mask: bool or uint8 [B*H, nb, nb] or [B, H, nb, nb], or one
+    [nb, nb] for every head (non-zero = kept, fractal block order; a row may keep
+    nothing), into ``workspace`` in sparse_attn_plan's format."""
+    nb = desc.T * desc.Hh * desc.Ww // desc.N
+    shapes = ((nb, nb), (desc.B * desc.H, nb, nb), (desc.B, desc.H, nb, nb))
+    if mask.dtype not in (torch.bool, torch.uint8) or not mask.is_cuda or \
+            not mask.is_contiguous() or tuple(mask.shape) not in shapes:
+        raise ValueError("mask must be a contiguous bool or uint8 CUDA tensor shaped [nb, nb], "
+                         "[B*H, nb, nb] or [B, H, nb, nb]")
+    heads = 1 if mask.dim() == 2 else desc.B * desc.H
+    _ok(lib().sparse_attn_plan_mask(ctypes.byref(desc), _ptr(mask), heads, _ptr(workspace),
+                                    workspace.numel(), _stream(stream)), "plan_mask")
+
+
+def relative_buckets(T: int, Hh: int, Ww: int, buckets=(16, 24, 24), max_distance=(32, 64, 64),
+                     device="cuda") -> Tuple[torch.Tensor, int]:
+    """(map, number of buckets) of a usual bucketing for ``fwd_bias``: per axis an
+    even number of buckets, half for each sign; offsets up to a quarter of them have
+    a bucket each, farther ones are spaced by the logarithm up to max_distance. Each
+    axis has its own buckets (t first). The map is int32 [(2T-1) + (2Hh-1) + (2Ww-1)]."""
+    out, base = [], 0
+    for n, b, far in zip((T, Hh, Ww), buckets, max_distance):
+        if b < 2 or b % 2 or far < 1:
+            raise ValueError("each axis needs an even number of buckets and a distance of 1 or more")
+        half = b // 2
+        exact = max(1, half // 2)
+        for off in range(-(n - 1), n):
+            a = abs(off)
+            if a >= exact:
+                step = math.log(a / exact) / math.log(far / exact) if far > exact else 1.0
+                a = min(half - 1, exact + int(step * (half - exact)))
+            out.append(base + a + (half if off > 0 else 0))
+        base += b
+    return torch.tensor(out, dtype=torch.int32, device=device), base
+
+
+def _rel_bias(desc: SaDesc, table: torch.Tensor, bucket: torch.Tensor) -> SaRelBias:
+    if table.dtype != torch.bfloat16 or not table.is_cuda or not table.is_contiguous() or \
+            table.dim() != 2 or table.shape[0] != desc.H:
+        raise ValueError("table must be a contiguous bf16 CUDA tensor shaped [H, buckets]")
+    n = 2 * (desc.T + desc.Hh + desc.Ww) - 3
+    if bucket.dtype != torch.int32 or not bucket.is_cuda or not bucket.is_contiguous() or \
+            tuple(bucket.shape) != (n,):
+        raise ValueError(f"bucket must be a contiguous int32 CUDA tensor of {n} offsets")
+    return SaRelBias(_ptr(table), _ptr(bucket), table.shape[1])
+
+
+def _check_like(name: str, t: torch.Tensor, dtype, shape) -> torch.Tensor:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+    return t
+
+
+def _same_device(q: torch.Tensor, *ts: Optional[torch.Tensor]) -> None:
+    """Every tensor on q's device, and that device current (its streams are)."""
+    for t in ts:
+        if t is not None and t.device != q.device:
+            raise ValueError(f"all tensors must be on q's device ({q.device}), got {t.device}")
+    if q.device.index != torch.cuda.current_device():
+        raise ValueError(f"q is on {q.device}, which is not the current device")
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An uninitialised tensor that belongs to the stream the call runs on, so that its
+    memory is not handed out again before the call is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device)
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def fwd_bias(desc: SaDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
+             bucket: torch.Tensor, workspace: torch.Tensor, out: Optional[torch.Tensor] = None,
+             lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """fwd with a learned relative position bias: ``table`` bf16 [H, buckets], ``bucket``
+    the int32 map of every offset (see ``relative_buckets``). ``lse`` (fp32 [B, H, S],
+    needed by ``bwd_bias``) is filled when given. Allocates ``out`` when None."""
+    _check_qkv(desc, q, k, v)
+    want = torch.float32 if desc.out_fp32 else torch.bfloat16
+    rel = _rel_bias(desc, table, bucket)
+    out = _check_like("out", _new(q.shape, want, q.device, stream) if out is None else out, want,
+                      q.shape)
+    if lse is not None:
+        _check_like("lse", lse, torch.float32, q.shape[:3])
+    _same_device(q, k, v, table, bucket, workspace, out, lse)
+    _ok(lib().sparse_attn_fwd_bias(ctypes.byref(desc), ctypes.byref(rel), _ptr(q), _ptr(k), _ptr(v),
+                                   _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse),
+                                   _stream(stream)), "fwd_bias")
+    return out
+
+
+def _grads(q: torch.Tensor, want, given, stream):
+    return [_check_like(n, _new(q.shape, want, q.device, stream) if g is None else g, want, q.shape)
+            for n, g in zip(("dq", "dk", "dv"), given)]
+
+
+def _score_scratch(desc: SaDesc, size_of, scratch, device, stream) -> torch.Tensor:
+    if scratch is not None:
+        return scratch
+    n = ctypes.c_size_t(0)
+    _ok(size_of(ctypes.byref(desc), ctypes.byref(n)), "bwd scratch size")
+    return _new(n.value, torch.uint8, device, stream)
+
+
+def bwd_bias(desc: SaDesc, q, k, v, table, bucket, out, dout, lse, workspace, dq=None, dk=None,
+             dv=None, dtable=None, scratch=None, stream=None):
+    """Gradients (dq, dk, dv, dtable) of sum(out * dout); ``out`` and ``lse`` are what
+    ``fwd_bias`` gave. Allocates the outputs and the scratch when None."""
+    _check_qkv(desc, q, k, v, dout)
+    want = torch.float32 if desc.out_fp32 else torch.bfloat16
+    rel = _rel_bias(desc, table, bucket)
+    _check_like("out", out, want, q.shape)
+    _check_like("lse", lse, torch.float32, q.shape[:3])
+    grads = _grads(q, want, (dq, dk, dv), stream)
+    grads.append(_check_like("dtable", _new(table.shape, want, q.device, stream)
+                             if dtable is None else dtable, want, table.shape))
+    scratch = _score_scratch(desc, lib().sparse_attn_bwd_bias_scratch_size, scratch, q.device, stream)
+    _same_device(q, k, v, table, bucket, workspace, out, dout, lse, scratch, *grads)
+    _ok(lib().sparse_attn_bwd_bias(ctypes.byref(desc), ctypes.byref(rel), _ptr(q), _ptr(k), _ptr(v),
+                                   _ptr(out), _ptr(dout), _ptr(lse), _ptr(workspace),
+                                   workspace.numel(), *[_ptr(g) for g in grads], _ptr(scratch),
+                                   scratch.numel(), _stream(stream)), "bwd_bias")
+    return tuple(grads)
+
+
+def _check_lam(desc: SaDesc, lam: torch.Tensor) -> None:
+    _check_like("lam", lam, torch.bfloat16, (desc.H,))
+
+
+def fwd_diff(desc: SaDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
+             workspace: torch.Tensor, out: Optional[torch.Tensor] = None,
+             out2: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+             stream=None) -> torch.Tensor:
+    """Differential attention over the plan: (P1 - lam P2) v with the maps of q's and
+    k's first and second half of the channels; ``lam`` bf16 [H]. ``out2`` (like out) and
+    ``lse`` (fp32 [2, B, H, S]), needed by ``bwd_diff``, are filled when given."""
+    _check_qkv(desc, q, k, v)
+    want = torch.float32 if desc.out_fp32 else torch.bfloat16
+    _check_lam(desc, lam)
+    out = _check_like("out", _new(q.shape, want, q.device, stream) if out is None else out, want,
+                      q.shape)
+    if out2 is not None:
+        _check_like("out2", out2, want, q.shape)
+    if lse is not None:
+        _check_like("lse", lse, torch.float32, (2,) + tuple(q.shape[:3]))
+    _same_device(q, k, v, lam, workspace, out, out2, lse)
+    _ok(lib().sparse_attn_fwd_diff(ctypes.byref(desc), _ptr(lam), _ptr(q), _ptr(k), _ptr(v),
+                                   _ptr(workspace), workspace.numel(), _ptr(out), _ptr(out2),
+                                   _ptr(lse), _stream(stream)), "fwd_diff")
+    return out
+
+
+def bwd_diff(desc: SaDesc, q, k, v, lam, out, out2, dout, lse, workspace, dq=None, dk=None,
+             dv=None, dlam=None, scratch=None, stream=None):
+    """Gradients (dq, dk, dv, dlam) of sum(out * dout); ``out``, ``out2`` and ``lse`` are
+    what ``fwd_diff`` gave. Allocates the outputs and the scratch when None."""
+    _check_qkv(desc, q, k, v, dout)
+    want = torch.float32 if desc.out_fp32 else torch.bfloat16
+    _check_lam(desc, lam)
+    _check_like("out", out, want, q.shape)
+    _check_like("out2", out2, want, q.shape)
+    _check_like("lse", lse, torch.float32, (2,) + tuple(q.shape[:3]))
+    grads = _grads(q, want, (dq, dk, dv), stream)
+    grads.append(_check_like("dlam", _new(lam.shape, want, q.device, stream)
+                             if dlam is None else dlam, want, lam.shape))
+    scratch = _score_scratch(desc, lib().sparse_attn_bwd_diff_scratch_size, scratch, q.device, stream)
+    _same_device(q, k, v, lam, workspace, out, out2, dout, lse, scratch, *grads)
+    _ok(lib().sparse_attn_bwd_diff(ctypes.byref(desc), _ptr(lam), _ptr(q), _ptr(k), _ptr(v),
+                                   _ptr(out), _ptr(out2), _ptr(dout), _ptr(lse), _ptr(workspace),
+                                   workspace.numel(), *[_ptr(g) for g in grads], _ptr(scratch),
+                                   scratch.numel(), _stream(stream)), "bwd_diff")
+    return tuple(grads)
 
 
 # ---- per-head block shapes (head-aware tiling) -------------------------------

@@ -181,9 +181,26 @@ const char* sparse_attn_plan_stage_name(int i) {
   return (i >= 0 && i < kNumPlanStages) ? kPlanStages[i] : nullptr;
 }
 
+// What the score functions other than q.k alone add to the attention call.
+struct Score {
+  BiasArgs bias;              // null table: none
+  const __nv_bfloat16* lam;   // differential: weights of the second map
+  void* out2;
+};
+
+// Arguments of a relative position bias; *args and the offset tables' limits.
+static sa_status check_bias(const sa_desc* desc, const sa_rel_bias* b, BiasArgs* args) {
+  if (b == nullptr || b->table == nullptr || b->bucket == nullptr || !aligned(b->table, 2) ||
+      !aligned(b->bucket, 4) || b->n_buckets < 1 || b->n_buckets > 4096)
+    return SA_ERR_INVALID_ARG;
+  if ((long long)desc->T + desc->Hh + desc->Ww > kRelBiasMaxAxes) return SA_ERR_UNSUPPORTED;
+  *args = {static_cast<const __nv_bfloat16*>(b->table), b->bucket, b->n_buckets, desc->H};
+  return SA_OK;
+}
+
 static sa_status fwd_impl(const sa_desc* desc, const void* q, const void* k, const void* v,
                           const void* workspace, size_t ws_bytes, void* out, float* lse,
-                          void* stream) {
+                          void* stream, const Score* score = nullptr) {
   sa_status st = validate(desc);
   if (st != SA_OK) return st;
   if (q == nullptr || k == nullptr || v == nullptr || out == nullptr || !aligned(q, 16) ||
@@ -211,6 +228,14 @@ static sa_status fwd_impl(const sa_desc* desc, const void* q, const void* k, con
   a.out_fp32 = desc->out_fp32;
   a.debug_flags = desc->debug_flags;
   a.lse = lse;
+  if (score != nullptr) {
+    a.bias = score->bias;
+    a.lam = score->lam;
+    a.out2 = score->out2;
+    a.H = desc->H;
+    if (a.lam != nullptr)
+      a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)(g.d / 2)));
+  }
   return cuda_status(launch_attn(a, g, static_cast<cudaStream_t>(stream)));
 }
 
@@ -382,6 +407,161 @@ sa_status sparse_attn_plan_radius(const sa_desc* desc, const sa_radius* radius,
   m.status = at<uint32_t>(workspace, w.status);
   if (launch_union(m, g, s) != cudaSuccess) return SA_ERR_CUDA;
   return cuda_status(launch_tile_order(m.tcnt, at<int32_t>(workspace, w.order), g, s));
+}
+
+sa_status sparse_attn_plan_mask(const sa_desc* desc, const uint8_t* mask, int mask_heads,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  sa_status st = validate(desc);
+  if (st != SA_OK) return st;
+  const Geometry g = make_geometry(*desc);
+  if (mask == nullptr || (mask_heads != 1 && mask_heads != g.BH)) return SA_ERR_INVALID_ARG;
+  st = check_ws(g, workspace, ws_bytes);
+  if (st != SA_OK) return st;
+  const WsLayout w = make_ws_layout(g);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(at<uint32_t>(workspace, w.status), 0, 256, s) != cudaSuccess)
+    return SA_ERR_CUDA;
+  MaskArgs m;
+  std::memset(&m, 0, sizeof(m));
+  m.bits = at<uint32_t>(workspace, w.bits);
+  m.cnt = at<int32_t>(workspace, w.cnt);
+  m.idx = at<int32_t>(workspace, w.idx);
+  m.tcnt = at<int32_t>(workspace, w.tcnt);
+  m.tidx = at<int32_t>(workspace, w.tidx);
+  m.status = at<uint32_t>(workspace, w.status);
+  const size_t head = mask_heads == 1 ? 0 : size_t(g.nb) * g.nb;
+  if (launch_mask_rows(mask, head, m.bits, m.cnt, m.idx, g, s) != cudaSuccess) return SA_ERR_CUDA;
+  if (launch_union(m, g, s) != cudaSuccess) return SA_ERR_CUDA;
+  return cuda_status(launch_tile_order(m.tcnt, at<int32_t>(workspace, w.order), g, s));
+}
+
+sa_status sparse_attn_fwd_bias(const sa_desc* desc, const sa_rel_bias* bias, const void* q,
+                               const void* k, const void* v, const void* workspace,
+                               size_t ws_bytes, void* out, float* lse, void* stream) {
+  sa_status st = validate(desc);
+  if (st != SA_OK) return st;
+  Score sc = {};
+  st = check_bias(desc, bias, &sc.bias);
+  if (st != SA_OK) return st;
+  if (lse != nullptr && !aligned(lse, 4)) return SA_ERR_INVALID_ARG;
+  return fwd_impl(desc, q, k, v, workspace, ws_bytes, out, lse, stream, &sc);
+}
+
+sa_status sparse_attn_fwd_diff(const sa_desc* desc, const void* lambda, const void* q,
+                               const void* k, const void* v, const void* workspace,
+                               size_t ws_bytes, void* out, void* out2, float* lse, void* stream) {
+  if (lambda == nullptr || !aligned(lambda, 2) || (out2 != nullptr && !aligned(out2, 16)) ||
+      (lse != nullptr && !aligned(lse, 4)))
+    return SA_ERR_INVALID_ARG;
+  Score sc = {};
+  sc.lam = static_cast<const __nv_bfloat16*>(lambda);
+  sc.out2 = out2;
+  return fwd_impl(desc, q, k, v, workspace, ws_bytes, out, lse, stream, &sc);
+}
+
+// Scratch of the gradients of either score function.
+static ScoreBwdLayout score_layout(const Geometry& g, bool diff) {
+  return make_score_bwd_layout(g, diff ? 2 : 1,
+                               diff ? 0 : size_t(g.ntile) * relbias_offsets(g));
+}
+
+// Gradients of a forward with a bias, or of differential attention (lambda given).
+static sa_status score_bwd_impl(const sa_desc* desc, const BiasArgs& bias, const void* lambda,
+                                const void* q, const void* k, const void* v, const void* out,
+                                const void* out2, const void* dout, const float* lse,
+                                const void* workspace, size_t ws_bytes, void* dq, void* dk,
+                                void* dv, void* dparam, void* scratch, size_t scratch_bytes,
+                                void* stream) {
+  const bool diff = lambda != nullptr;
+  const void* ptrs[] = {q, k, v, out, dout, dq, dk, dv, scratch};
+  for (const void* p : ptrs)
+    if (p == nullptr || !aligned(p, 16)) return SA_ERR_INVALID_ARG;
+  if (diff && (out2 == nullptr || !aligned(out2, 16))) return SA_ERR_INVALID_ARG;
+  if (lse == nullptr || !aligned(lse, 4) || dparam == nullptr || !aligned(dparam, 4))
+    return SA_ERR_INVALID_ARG;
+  const Geometry g = make_geometry(*desc);
+  sa_status st = check_ws(g, workspace, ws_bytes);
+  if (st != SA_OK) return st;
+  const ScoreBwdLayout b = score_layout(g, diff);
+  if (scratch_bytes < b.total) return SA_ERR_WORKSPACE;
+  if (!aligned(scratch, 256)) return SA_ERR_INVALID_ARG;
+  const WsLayout w = make_ws_layout(g);
+  ScoreBwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (!encode_tile_map(&a.map_q, q, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
+      !encode_tile_map(&a.map_k, k, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
+      !encode_tile_map(&a.map_v, v, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
+      !encode_tile_map(&a.map_do, dout, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw))
+    return SA_ERR_CUDA;
+  a.out = out;
+  a.out2 = out2;
+  a.dout = static_cast<const __nv_bfloat16*>(dout);
+  a.lse = lse;
+  a.lse2 = at<float>(scratch, b.lse2);
+  a.dsum = at<float>(scratch, b.dsum);
+  a.part = at<float>(scratch, b.part);
+  a.kcnt = at<int32_t>(scratch, b.kcnt);
+  a.kidx = at<int32_t>(scratch, b.kidx);
+  a.bits = at<uint32_t>(workspace, w.bits);
+  a.tcnt = at<int32_t>(workspace, w.tcnt);
+  a.tidx = at<int32_t>(workspace, w.tidx);
+  a.order = at<int32_t>(workspace, w.order);
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dparam = dparam;
+  a.bias = bias;
+  a.lam = static_cast<const __nv_bfloat16*>(lambda);
+  a.H = desc->H;
+  a.status = const_cast<uint32_t*>(at<uint32_t>(workspace, w.status));
+  const double scale = 1.0 / std::sqrt((double)(diff ? g.d / 2 : g.d));
+  a.scale_log2 = (float)(1.4426950408889634 * scale);
+  a.scale = (float)scale;
+  a.out_fp32 = desc->out_fp32;
+  a.debug_flags = desc->debug_flags;
+  return cuda_status(launch_score_bwd(a, g, static_cast<cudaStream_t>(stream)));
+}
+
+sa_status sparse_attn_bwd_bias_scratch_size(const sa_desc* desc, size_t* bytes) {
+  const sa_status st = validate(desc);
+  if (st != SA_OK) return st;
+  if (bytes == nullptr) return SA_ERR_INVALID_ARG;
+  *bytes = score_layout(make_geometry(*desc), false).total;
+  return SA_OK;
+}
+
+sa_status sparse_attn_bwd_bias(const sa_desc* desc, const sa_rel_bias* bias, const void* q,
+                               const void* k, const void* v, const void* out, const void* dout,
+                               const float* lse, const void* workspace, size_t ws_bytes, void* dq,
+                               void* dk, void* dv, void* dtable, void* scratch,
+                               size_t scratch_bytes, void* stream) {
+  sa_status st = validate(desc);
+  if (st != SA_OK) return st;
+  BiasArgs b;
+  st = check_bias(desc, bias, &b);
+  if (st != SA_OK) return st;
+  return score_bwd_impl(desc, b, nullptr, q, k, v, out, nullptr, dout, lse, workspace, ws_bytes, dq,
+                        dk, dv, dtable, scratch, scratch_bytes, stream);
+}
+
+sa_status sparse_attn_bwd_diff_scratch_size(const sa_desc* desc, size_t* bytes) {
+  const sa_status st = validate(desc);
+  if (st != SA_OK) return st;
+  if (bytes == nullptr) return SA_ERR_INVALID_ARG;
+  *bytes = score_layout(make_geometry(*desc), true).total;
+  return SA_OK;
+}
+
+sa_status sparse_attn_bwd_diff(const sa_desc* desc, const void* lambda, const void* q,
+                               const void* k, const void* v, const void* out, const void* out2,
+                               const void* dout, const float* lse, const void* workspace,
+                               size_t ws_bytes, void* dq, void* dk, void* dv, void* dlambda,
+                               void* scratch, size_t scratch_bytes, void* stream) {
+  const sa_status st = validate(desc);
+  if (st != SA_OK) return st;
+  if (lambda == nullptr || !aligned(lambda, 2)) return SA_ERR_INVALID_ARG;
+  return score_bwd_impl(desc, BiasArgs{}, lambda, q, k, v, out, out2, dout, lse, workspace,
+                        ws_bytes, dq, dk, dv, dlambda, scratch, scratch_bytes, stream);
 }
 
 sa_status sparse_attn_permute(const sa_desc* desc, const void* x, void* y, int inverse,

@@ -34,6 +34,17 @@
 // when the softmax of tile X sees S_X(j) complete, PV_X(j-1) (issued before
 // S_X(j)) is complete too, and O_X may be rescaled without another wait.
 //
+// Two more forms of the same kernel (template parameter M):
+//   bias  s gets a learned relative position bias before the softmax: the head's
+//         three offset tables (log2 units) lie in shared memory, and a thread
+//         adds one value per key row and one per key column of the block.
+//   diff  differential attention, O = P_1 V - lambda P_2 V: tiles A and B are
+//         the two maps of ONE query tile (channels [0, d/2) and [d/2, d) of q
+//         and k), so S_X takes K = d/2 and both maps run the same list; the
+//         epilogue joins O_A and O_B in TMEM, half of the columns per map's warps.
+// A tile whose rows keep nothing (only a caller's own mask has such) writes
+// zeros and a log-sum-exp of -inf.
+//
 // All waits are bounded (sm100.cuh); a wait that runs out records a status
 // bit, raises a CTA-wide abort flag, drains its own in-flight work and lets
 // the CTA free TMEM and exit.
@@ -42,6 +53,7 @@
 
 #include "exp2_poly.cuh"
 #include "kernels.cuh"
+#include "relbias.cuh"
 #include "sm100.cuh"
 
 namespace sa {
@@ -78,6 +90,12 @@ constexpr int kMaxList = 2880;
 
 __host__ __device__ constexpr uint32_t col_s(int x) { return uint32_t(x) * 128u; }
 __host__ __device__ constexpr uint32_t col_o(int x) { return 256u + uint32_t(x) * 128u; }
+
+// What the bias and diff forms keep behind AttnSmem.
+struct DiffSmem {
+  float inv[2][128];  // 1 / l of each map's rows
+  uint64_t inv_full;
+};
 
 template <int D>
 struct __align__(1024) AttnSmem {
@@ -161,18 +179,54 @@ __device__ __forceinline__ int s_op_index(int x, int step, int n0, int n1) {
   return x == 0 ? base + 1 : base + (i < n0) + (i + 1 < n0) + 1;
 }
 
+// 32 columns of O times `inv`, or zeros when the tile ran no step.
+__device__ __forceinline__ void load_o32(uint32_t col, int nsteps, float inv, float (&x)[32]) {
+  if (nsteps > 0) {
+    uint32_t o[32];
+    tmem_ld32(col, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = 0.f;
+  }
+}
+
+// 32 values -> elements [at, at + 32) of an output, bf16 or fp32.
+__device__ __forceinline__ void store_o32(void* out, size_t at, const float (&x)[32], int fp32) {
+  if (fp32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at);
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      dst[v] = make_uint4(pack_bf16x2(x[8 * v], x[8 * v + 1]),
+                          pack_bf16x2(x[8 * v + 2], x[8 * v + 3]),
+                          pack_bf16x2(x[8 * v + 4], x[8 * v + 5]),
+                          pack_bf16x2(x[8 * v + 6], x[8 * v + 7]));
+  }
+}
+
 __device__ __forceinline__ int step_blocks(const Tile& t, int step) {
   return (t.n_u - 2 * step) >= 2 ? 2 : 1;
 }
 
 }  // namespace
 
-template <int D>
+template <int D, AttnMode M>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ AttnArgs a, const Geometry g) {
   extern __shared__ uint8_t smem_raw[];
   AttnSmem<D>& sm = *reinterpret_cast<AttnSmem<D>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr bool kDiff = M == AttnMode::kDiff;
+  constexpr bool kBias = M == AttnMode::kBias || M == AttnMode::kBias8;
+  DiffSmem& df = *reinterpret_cast<DiffSmem*>(&sm + 1);   // diff only
+  float* bias = reinterpret_cast<float*>(&sm + 1);        // bias only
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y;
   const int pair = blockIdx.x;
@@ -184,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Tile tile[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int pos = 2 * pair + x;  // position in the head's tile order
+    // position in the head's tile order
+    const int pos = kDiff ? pair : 2 * pair + x;
     tile[x].qa = tile[x].qb = -1;
     tile[x].n_u = tile[x].nsteps = 0;
     tile[x].list = nullptr;
@@ -198,10 +253,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile[x].glist = src;
       // every warp reads the lists at each step: stage them in shared memory
       const int staged = tile[x].n_u < kMaxList ? tile[x].n_u : kMaxList;
-      for (int i = threadIdx.x; i < staged; i += kThreads) sm.list[x][i] = src[i];
+      if (!kDiff || x == 0)
+        for (int i = threadIdx.x; i < staged; i += kThreads) sm.list[x][i] = src[i];
     }
-    tile[x].list = sm.list[x];
+    tile[x].list = sm.list[kDiff ? 0 : x];
   }
+  if constexpr (kBias) relbias_load(bias, a.bias, g, bh, threadIdx.x, kThreads, a.status);
   volatile int* abort = &sm.abort;
 
   if (threadIdx.x == 0) {
@@ -216,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.empty[s], 1);
     }
     mbar_init(&sm.drain, 1);
+    if constexpr (kDiff) mbar_init(&df.inv_full, 256);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -246,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&a.map_v2);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (tile[x].nsteps == 0) continue;
+          if (tile[x].nsteps == 0 || (kDiff && x == 1)) continue;
           mbar_arrive_expect_tx(&sm.q_full[x], 128u * D * 2u);
           for (int e = 0; e < 2; ++e) {
             const int blk = (e == 0 || tile[x].qb < 0) ? tile[x].qa : tile[x].qb;
@@ -277,14 +335,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const Tile t = x ? tile[1] : tile[0];
         const int nblk = step_blocks(t, step);
-        mbar_arrive_expect_tx(&sm.full[s], uint32_t(nblk) * 64u * D * 2u);
+        // channel chunks of the op: a differential map's S needs its own half
+        const bool half_k = kDiff && D == 128 && kind == 0;
+        const int c_lo = half_k ? x : 0, c_hi = half_k ? x + 1 : D / 64;
+        mbar_arrive_expect_tx(&sm.full[s], uint32_t(nblk) * 64u * uint32_t(c_hi - c_lo) * 128u);
         const int e0 = list_at(t, 2 * step);
         if (nblk == 2 && (e0 & kEntryTPair) && (e0 & kEntryBlockMask) + g.nh * g.nw < g.nb) {
           // the same patch in frames t, t+1: one two-frame box per channel half
           int tt, hp, wp;
           block_coords(g, e0 & kEntryBlockMask, tt, hp, wp);
           const CUtensorMap* map = kind == 0 ? &a.map_k2 : &a.map_v2;
-          for (int c = 0; c < D / 64; ++c)
+          for (int c = c_lo; c < c_hi; ++c)
             tma_load_5d(&sm.slot[s][c][0], map, &sm.full[s], c * 64, wp * g.pw, hp * g.ph, tt * g.pt, bh);
         } else {
           const CUtensorMap* map = kind == 0 ? &a.map_k : &a.map_v;
@@ -296,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             int tt, hp, wp;
             block_coords(g, kb, tt, hp, wp);
-            for (int c = 0; c < D / 64; ++c)
+            for (int c = c_lo; c < c_hi; ++c)
               tma_load_5d(&sm.slot[s][c][e * 8192], map, &sm.full[s], c * 64, wp * g.pw, hp * g.ph,
                           tt * g.pt, bh);
           }
@@ -333,8 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kSlotStep = (D / 64) * kChunkBytes / 16;  // one slot, 16 B units
       const int n0 = tile[0].nsteps, n1 = tile[1].nsteps;
       const int u0 = tile[0].n_u, u1 = tile[1].n_u;
-      bool ok = mbar_wait(&sm.q_full[0], 0, abort);
-      if (ok && n1 > 0) ok = mbar_wait(&sm.q_full[1], 0, abort);
+      bool ok = n0 == 0 || mbar_wait(&sm.q_full[0], 0, abort);  // (heaviest first: n1 <= n0)
+      if (!kDiff && ok && n1 > 0) ok = mbar_wait(&sm.q_full[1], 0, abort);
       int k = 0;  // op index (ring position)
 #if SA_TRACE
       int tr_u = 0;
@@ -345,7 +406,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t kd = kdesc0 + uint64_t(s) * kSlotStep;
         const uint32_t id = ((x ? u1 : u0) - 2 * step) >= 2 ? id_s2 : id_s1;
         const uint32_t d_tmem = tmem + col_s(x);
-        if constexpr (D == 128) {
+        if constexpr (kDiff) {
+          // map x: K steps of channels [x D/2, (x + 1) D/2) of the one Q tile
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) {
+            const int ks = x * (D / 32) + kk;
+            const uint32_t off = (uint32_t(ks >> 2) * kChunkBytes + uint32_t(ks & 3) * 32u) >> 4;
+            mma_ss(d_tmem, qdesc0 + off, kd + off, id, kk > 0);
+          }
+        } else if constexpr (D == 128) {
           mma_ss_k8<kChunkBytes>(d_tmem, qd, kd, id, 0u);
         } else {
 #pragma unroll
@@ -450,6 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    RelBiasRow rb;
+    if constexpr (kBias) rb = relbias_row(g, half && t.qb >= 0 ? t.qb : t.qa, r & 63, 1);
     for (int j = 0; j < t.nsteps; ++j) {
       const int nblk = step_blocks(t, j);
       const int e0 = list_at(t, 2 * j);
@@ -477,6 +548,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(s_col + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
       }
       tmem_wait_ld();
+      if constexpr (kBias) {
+        // log2 units, bias included, before the maximum is taken
+        if (keep0) relbias_add64<M == AttnMode::kBias8>(bias, rb, g, e0 & kEntryBlockMask, sl2, &sv[0]);
+        if (keep1) relbias_add64<M == AttnMode::kBias8>(bias, rb, g, e1 & kEntryBlockMask, sl2, &sv[64]);
+      }
       // row max over four independent chains (a single chain of 64 dependent
       // max3 would cost its full latency)
       float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -491,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mq[(i >> 1) & 3] = max3(mq[(i >> 1) & 3], __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
       }
       float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-      mx *= sl2;
+      if constexpr (!kBias) mx *= sl2;
       const bool need = mx > m + kRescaleThreshold;  // false while mx = -inf
       const float m_new = need ? mx : m;
       const float alpha = need ? ex2_approx(m - m_new) : 1.f;  // m = -inf -> 0
@@ -512,16 +588,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // p = 2^(s * log2(e)/sqrt(d) - m), two columns per packed op;
       // kPolyPairsPer8 of every 8 column pairs take the FMA-pipe exp2.
       const uint64_t sl2x2 = f2_pack(sl2, sl2);
-      const uint64_t negm2 = f2_pack(-m, -m);
+      // (bias: a row whose offsets are all masked so far has m = -inf; p = 2^-inf = 0)
+      const float negm = kBias && m == -INFINITY ? 0.f : -m;
+      const uint64_t negm2 = f2_pack(negm, negm);
       uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};  // four independent packed sums
 #pragma unroll
       for (int i = 0; i < 64; ++i) {
         const bool kp = (2 * i) < 64 ? keep0 : keep1;
         uint32_t packed = 0u;
         if (kp) {
-          const uint64_t x2 =
-              f2_fma(f2_pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sl2x2,
-                     negm2);
+          const uint64_t s2 = f2_pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+          const uint64_t x2 = kBias ? f2_add(s2, negm2) : f2_fma(s2, sl2x2, negm2);
           float x0, x1;
           f2_unpack(x2, x0, x1);
           uint64_t e2;
@@ -551,61 +628,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         g_attn_trace[kTraceSoftmax + (warp - 4) * 2 * kTraceSteps + 2 * j + 1] = clock64();
 #endif
     }
-    if (t.nsteps > 0) {
-      if (!ok) {
+    // ---- epilogue: O / l -> natural token position
+    if (!ok) {
+      fail(a.status, &sm.abort, kDevErrTimeoutSoftmax);
+    } else {
+      const float inv = l > 0.f ? 1.0f / l : 0.f;
+      bool done = t.nsteps == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&sm.o_final[x], 0, abort));
+      if constexpr (kDiff) {
+        // the rows of both maps meet here: 1 / l of each, then both O's in TMEM
+        df.inv[x][r] = inv;
+        mbar_arrive(&df.inv_full);
+        done = done && __all_sync(0xFFFFFFFFu, mbar_wait(&df.inv_full, 0, abort)) &&
+               (t.nsteps == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&sm.o_final[x ^ 1], 0, abort)));
+      }
+      if (!done) {
         fail(a.status, &sm.abort, kDevErrTimeoutSoftmax);
-      } else if (__all_sync(0xFFFFFFFFu, mbar_wait(&sm.o_final[x], 0, abort))) {
+      } else if (t.qa >= 0 && (half == 0 || t.qb >= 0)) {  // uniform across the warp
         tc_fence_after_sync();
-        // ---- epilogue: O / l -> natural token position
-        if (row_valid) {
-          const int blk = half ? t.qb : t.qa;
-          int tt, hp, wp;
-          block_coords(g, blk, tt, hp, wp);
-          // row i of the block: frame tt*pt + (i >> (lph + lpw)), row
-          // hp*ph + ((i >> lpw) & (ph - 1)), column wp*pw + (i & (pw - 1))
-          const int i = r & 63;
-          const int run = i >> g.lpw;
-          const size_t tok = (size_t(tt) * g.pt + (run >> g.lph)) * g.Hh * g.Ww +
-                             size_t(hp * g.ph + (run & (g.ph - 1))) * g.Ww +
-                             size_t(wp * g.pw + (i & (g.pw - 1)));
-          const size_t row = size_t(bh) * g.S + tok;
-          const float inv = l > 0.f ? 1.0f / l : 0.f;
-          // log-sum-exp of the row's kept scaled scores (natural log): m is
-          // in log2 units and l is the sum relative to 2^m
-          if (a.lse != nullptr)
-            a.lse[row] = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+        const size_t row = size_t(bh) * g.S + block_row_token(g, half ? t.qb : t.qa, r & 63);
+        // log-sum-exp of the row's kept scaled scores (natural log): m is
+        // in log2 units and l is the sum relative to 2^m
+        if (a.lse != nullptr)
+          a.lse[row + (kDiff ? size_t(x) * g.BH * g.S : 0)] =
+              l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+        if constexpr (kDiff) {
+          // this map's warps write half of the channels of out and out2
+          const float inv1 = df.inv[0][r], inv2 = df.inv[1][r];
+          const float lam = __bfloat162float(a.lam[bh % a.H]);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const int col = x * (D / 2) + 32 * c;
+            float o1[32], o2[32];
+            load_o32(t_lane + col_o(0) + uint32_t(col), t.nsteps, inv1, o1);
+            load_o32(t_lane + col_o(1) + uint32_t(col), t.nsteps, inv2, o2);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o1[i] = fmaf(-lam, o2[i], o1[i]);
+            store_o32(a.out, row * D + col, o1, a.out_fp32);
+            if (a.out2 != nullptr) store_o32(a.out2, row * D + col, o2, a.out_fp32);
+          }
+        } else {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(o_col + 32 * c, o);
-            tmem_wait_ld();
-            if (a.out_fp32) {
-              float4* dst =
-                  reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + 32 * c);
-#pragma unroll
-              for (int v4 = 0; v4 < 8; ++v4)
-                dst[v4] = make_float4(__uint_as_float(o[4 * v4]) * inv,
-                                      __uint_as_float(o[4 * v4 + 1]) * inv,
-                                      __uint_as_float(o[4 * v4 + 2]) * inv,
-                                      __uint_as_float(o[4 * v4 + 3]) * inv);
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D +
-                                                    32 * c);
-#pragma unroll
-              for (int v8 = 0; v8 < 4; ++v8)
-                dst[v8] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * v8]) * inv,
-                                                 __uint_as_float(o[8 * v8 + 1]) * inv),
-                                     pack_bf16x2(__uint_as_float(o[8 * v8 + 2]) * inv,
-                                                 __uint_as_float(o[8 * v8 + 3]) * inv),
-                                     pack_bf16x2(__uint_as_float(o[8 * v8 + 4]) * inv,
-                                                 __uint_as_float(o[8 * v8 + 5]) * inv),
-                                     pack_bf16x2(__uint_as_float(o[8 * v8 + 6]) * inv,
-                                                 __uint_as_float(o[8 * v8 + 7]) * inv));
-            }
+            float o[32];
+            load_o32(o_col + 32 * c, t.nsteps, inv, o);
+            store_o32(a.out, row * D + 32 * c, o, a.out_fp32);
           }
         }
-      } else {
-        fail(a.status, &sm.abort, kDevErrTimeoutSoftmax);
       }
     }
   }
@@ -616,18 +684,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D>
-static cudaError_t launch_attn_d(const AttnArgs& a, const Geometry& g, cudaStream_t stream) {
+template <int D, AttnMode M>
+static cudaError_t launch_attn_m(const AttnArgs& a, const Geometry& g, cudaStream_t stream) {
   // At least 120 KB so that one CTA occupies an SM: each CTA allocates all
   // 512 TMEM columns.
-  const size_t need = sizeof(AttnSmem<D>) + 1024;
+  size_t need = sizeof(AttnSmem<D>) + 1024;
+  if (M == AttnMode::kBias || M == AttnMode::kBias8) need += relbias_offsets(g) * sizeof(float);
+  if (M == AttnMode::kDiff) need += sizeof(DiffSmem);
   const size_t smem = need > 120 * 1024 ? need : 120 * 1024;
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       int(smem));
+  cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, M>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  const dim3 grid(unsigned((g.ntile + 1) / 2), unsigned(g.BH));
-  attn_kernel<D><<<grid, kThreads, smem, stream>>>(a, g);
+  const dim3 grid(unsigned(M == AttnMode::kDiff ? g.ntile : (g.ntile + 1) / 2), unsigned(g.BH));
+  attn_kernel<D, M><<<grid, kThreads, smem, stream>>>(a, g);
   return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_attn_d(const AttnArgs& a, const Geometry& g, cudaStream_t stream) {
+  if (a.lam != nullptr) return launch_attn_m<D, AttnMode::kDiff>(a, g, stream);
+  if (a.bias.table == nullptr) return launch_attn_m<D, AttnMode::kPlain>(a, g, stream);
+  return g.lpw == 3 ? launch_attn_m<D, AttnMode::kBias8>(a, g, stream)
+                    : launch_attn_m<D, AttnMode::kBias>(a, g, stream);
 }
 
 cudaError_t launch_attn(const AttnArgs& a, const Geometry& g, cudaStream_t stream) {

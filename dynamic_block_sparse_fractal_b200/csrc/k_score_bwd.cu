@@ -1,0 +1,855 @@
+// Gradients of the block-sparse attention with another score function: a
+// learned relative position bias (one map) or differential attention (two maps
+// that share the values, out = (P_1 - lambda P_2) V).
+//
+// With z the scores, P_m = 2^(z_m - lse_m) from the forward's row statistics,
+// dP = dO V^T and D_m = rowsum(dO * P_m V):
+//   dV = Pc^T dO            Pc = P (bias), P_1 - lambda P_2 (differential)
+//   dS_1 = P_1 (dP - D_1),  dS_2 = -lambda P_2 (dP - D_2)
+//   dQ_m = dS_m K_m * scale, dK_m = dS_m^T Q_m * scale
+//   dtable[b] = sum of dS over the pairs in bucket b;  dlambda = -sum D_2
+//
+// Two tensor-core passes that each rebuild P and dP, instead of one pass that
+// reduces dQ into memory: the query pass keeps a query tile and runs over its
+// union list (dQ), the key pass keeps a key tile and runs over the q-blocks that
+// keep it (dK, dV, dtable). Two products and the exponentials are done twice (8
+// units of 2 N^2 d per kept pair instead of 5), but there are no atomics on dQ
+// (the same bits at every run) and no fp32 accumulator to clear, reduce into and
+// convert, and TMEM has room for two stages of scores, so that the products of
+// one step run while the row warps work on the other.
+//
+// D. rowsum(dO * O) of a stored bf16 output carries its rounding, and the error
+// of D is common to a whole row of dS. The query pass therefore starts from that
+// value D~ (dS~ = P (dP - D~)), sums D = rowsum(P * dP) in fp32 on the way, and
+// corrects dQ = dS~ K - (D - D~) P K at the end with one more product, P K; the
+// key pass reads the corrected D. (With D~ alone dQ was 4.5e-3 off in the 2-norm
+// and the parameters' gradients up to 7e-3.)
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kernels.cuh"
+#include "relbias.cuh"
+#include "sm100.cuh"
+
+namespace sa {
+
+namespace {
+
+constexpr int kSbThreads = 640;   // warps 0, 2 TMA, 1 MMA, 3 idle; 4-19 rows
+constexpr int kSbRowWarps = 16;   // two groups of 8: the even and the odd steps; in a group two
+                                  // warpgroups of 128 rows, half of a step's columns each
+constexpr int kSbList = 2880;     // list entries staged in shared memory (the rest from L2)
+constexpr int kSbSlots = 4;       // ring of streamed blocks
+constexpr int kTile = 128 * 128;  // 128 rows x 128 B (64 bf16 channels)
+constexpr int kBlk = 64 * 128;    // 64 rows x 128 B
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void fail_s(uint32_t* status, int* abort, uint32_t bit) {
+  atomicOr(status, bit);
+  *reinterpret_cast<volatile int*>(abort) = 1;
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// One arrival for a warp whose lanes have all finished their TMEM accesses
+// (tcgen05.wait before the call).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  tc_fence_before_sync();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// A and B both K-major, one accumulator of 128 x N: NK K steps of 16 channels
+// from step k0 on; a_chunk / b_chunk bytes between 64-channel chunks.
+template <int NK>
+__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint64_t a, uint32_t a_chunk,
+                                           uint64_t b, uint32_t b_chunk, uint32_t id, int k0) {
+#pragma unroll
+  for (int kk = 0; kk < NK; ++kk) {
+    const int ks = k0 + kk;
+    const uint32_t in = uint32_t(ks & 3) * 32u;
+    mma_ss(d_tmem, a + ((uint32_t(ks >> 2) * a_chunk + in) >> 4),
+           b + ((uint32_t(ks >> 2) * b_chunk + in) >> 4), id, kk > 0);
+  }
+}
+
+// A from TMEM, NK K steps 16 columns apart; B an MN-major block (16 rows a step).
+template <int NK>
+__device__ __forceinline__ void mma_from_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                              uint32_t id, uint32_t acc) {
+#pragma unroll
+  for (int kk = 0; kk < NK; ++kk)
+    mma_ts(d_tmem, a_tmem + uint32_t(kk) * 16u, b + uint64_t(kk) * 128u, id, kk > 0 ? 1u : acc);
+}
+
+// mul * (32 accumulator columns of this lane's row - fix * 32 columns at `sub`)
+// (zeros without a step) -> 32 elements of an output, bf16 or fp32.
+__device__ __forceinline__ void store_acc32(uint32_t col, uint32_t sub, bool any, float mul,
+                                            float fix, void* out, size_t at, int fp32) {
+  float x[32];
+  if (any) {
+    uint32_t o[32];
+    tmem_ld32(col, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
+    if (sub != 0u) {
+      tmem_ld32(sub, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = fmaf(-fix, __uint_as_float(o[i]), x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] *= mul;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = 0.f;
+  }
+  if (fp32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at);
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      dst[v] = make_uint4(pack_bf16x2(x[8 * v], x[8 * v + 1]),
+                          pack_bf16x2(x[8 * v + 2], x[8 * v + 3]),
+                          pack_bf16x2(x[8 * v + 4], x[8 * v + 5]),
+                          pack_bf16x2(x[8 * v + 6], x[8 * v + 7]));
+  }
+}
+
+// TMEM column, relative to a [128 x d] accumulator, of output channel c (a
+// multiple of 32): with two maps of 32 channels each map's product is taken over
+// all 64 channels of the block, 64 columns apart, and half of it is used.
+template <int D, bool kDiff>
+__device__ __forceinline__ uint32_t acc_col(int c) {
+  return uint32_t(kDiff && D == 64 && c >= 32 ? 64 + c : c);
+}
+
+// The bias of a row warp's 32 columns of a block, c = 32 wg + ..: with L =
+// min(log2 pw, 5) it is f[c >> L] + g[c & (2^L - 1)], f from the time and row
+// tables and g from the column table.
+template <int L>
+struct Cols {
+  static constexpr int kG = 1 << L, kF = 32 >> L;
+};
+
+template <int L>
+__device__ __forceinline__ int f_run(const Geometry& g, int wg, int x) {
+  return (32 * wg + x * Cols<L>::kG) >> g.lpw;
+}
+template <int L>
+__device__ __forceinline__ int g_col(const Geometry& g, int wg, int y) {
+  return (32 * wg + y) & (g.pw - 1);
+}
+
+template <int L>
+__device__ __forceinline__ void load_bias32(const float* bias, const Geometry& g, int t, int h,
+                                            int w, int wg, int sign, float (&f)[Cols<L>::kF],
+                                            float (&c)[Cols<L>::kG]) {
+#pragma unroll
+  for (int x = 0; x < Cols<L>::kF; ++x) {
+    const int run = f_run<L>(g, wg, x);
+    f[x] = bias[t + sign * (run >> g.lph)] + bias[h + sign * (run & (g.ph - 1))];
+  }
+#pragma unroll
+  for (int y = 0; y < Cols<L>::kG; ++y) c[y] = bias[w + sign * g_col<L>(g, wg, y)];
+}
+
+// Sums N values of each lane over the lanes that differ in lane bits [LO, HI):
+// while more than one value is left a bit halves them between the two lanes,
+// after that it sums. Returns how many are left in v[0..); `first` is the index
+// of v[0] among the N, and `writer` is false where another lane holds the same.
+template <int N, int LO, int HI>
+__device__ __forceinline__ int lane_sums(float (&v)[N], int lane, int& first, bool& writer) {
+  int n = N;
+  first = 0;
+  writer = true;
+#pragma unroll
+  for (int bit = HI - 1; bit >= LO; --bit) {
+    const bool up = (lane >> bit) & 1;
+    if (n > 1) {
+      n >>= 1;
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) {
+        if (k < n) {
+          const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
+          v[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, 1 << bit);
+        }
+      }
+      first += up ? n : 0;
+    } else {
+      v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 1 << bit);
+      writer = writer && !up;
+    }
+  }
+  return n;
+}
+
+// dS of this thread's key against 32 query columns of a block, already summed
+// over each run (f) and each column (c), added to the CTA's histogram over
+// offsets (the layout of the bias tables; t, h, w: the block's indexes). Lanes of
+// a warp are 32 tokens of one block: their low L bits are the column. Sums over
+// the lanes that share an address come first, so that a warp issues a few
+// additions with few conflicts.
+template <int L>
+__device__ __forceinline__ void add_table_grad(float* hist, const Geometry& g, int t, int h, int w,
+                                               int wg, int lane, float (&f)[Cols<L>::kF],
+                                               float (&c)[Cols<L>::kG]) {
+  constexpr int NG = Cols<L>::kG, NF = Cols<L>::kF;
+  if (g.pt == 1) {  // one frame offset for the whole warp
+    float s = 0.f;
+#pragma unroll
+    for (int x = 0; x < NF; ++x) s += f[x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == 0) atomicAdd(hist + t, s);
+  }
+  int first;
+  bool writer;
+  int n = lane_sums<NF, 0, L>(f, lane, first, writer);  // lanes of one row run
+  if (writer) {
+#pragma unroll
+    for (int k = 0; k < NF; ++k) {
+      if (k >= n) break;
+      const int run = f_run<L>(g, wg, first + k);
+      if (g.pt != 1) atomicAdd(hist + t - (run >> g.lph), f[k]);
+      atomicAdd(hist + h - (run & (g.ph - 1)), f[k]);
+    }
+  }
+  n = lane_sums<NG, L, 5>(c, lane, first, writer);  // lanes of one column
+  if (writer) {
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      if (k >= n) break;
+      atomicAdd(hist + w - g_col<L>(g, wg, first + k), c[k]);
+    }
+  }
+}
+
+// What a CTA of either pass streams and waits on.
+struct SbBars {
+  uint64_t tile_full, full[kSbSlots], empty[kSbSlots];
+  uint64_t s_full[2], out_full[2], acc_full, dsum_full, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+struct __align__(1024) SbSmem {
+  uint8_t ta[D / 64][kTile], tb[D / 64][kTile];               // the tile's K, V (or Q, dO)
+  uint8_t sa[kSbSlots][D / 64][kBlk], sb[kSbSlots][D / 64][kBlk];  // streamed Q, dO (or K, V)
+  float lse2[kSbSlots][2][64], dsum[kSbSlots][2][64];         // of streamed query rows, per map
+  int32_t list[kSbList];
+  SbBars bar;
+};
+// (the query pass sums each row's D over four warps in the statistics' place)
+// with the offset tables and the histogram of the largest grid, a CTA's 227 KB
+static_assert(sizeof(SbSmem<128>) + 1024 + 2 * sizeof(float) * (2 * kRelBiasMaxAxes - 3) <= 232448,
+              "shared memory of the gradient passes");
+
+}  // namespace
+
+// D_m and lse_m * log2(e) of every row into fractal order (an empty row's
+// lse = -inf becomes +inf, so that 2^(z - lse) is 0). D/8 lanes per row, 128 rows
+// per CTA, one head per CTA.
+constexpr int kPrepRows = 128;
+
+template <int D, bool kDiff>
+__global__ void __launch_bounds__(256)
+    score_prep_kernel(const void* __restrict__ o, const void* __restrict__ o2,
+                      const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse,
+                      const __nv_bfloat16* __restrict__ lam, int H, float* __restrict__ lse2,
+                      float* __restrict__ dsum, int fp32, Geometry g) {
+  constexpr int kLanes = D / 8;
+  const int sub = threadIdx.x % kLanes, bh = blockIdx.y;
+  const size_t all = size_t(g.BH) * g.S;
+  const float lm = kDiff ? __bfloat162float(lam[bh % H]) : 0.f;
+  for (int i = threadIdx.x / kLanes; i < kPrepRows; i += 256 / kLanes) {
+    const int pos = blockIdx.x * kPrepRows + i;
+    if (pos >= g.S) break;
+    const size_t row = size_t(bh) * g.S + block_row_token(g, pos >> 6, pos & 63);
+    const size_t at = row * D + 8 * sub;
+    const uint4 dv = __ldg(reinterpret_cast<const uint4*>(dout + at));
+    auto dot = [&](const void* p) {
+      float acc = 0.f;
+      const uint32_t* dw = &dv.x;
+      if (fp32) {
+        const float4* x = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+        const float4 a = __ldg(x), b = __ldg(x + 1);
+        const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 d = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(dw + w));
+          acc += d.x * y[2 * w] + d.y * y[2 * w + 1];
+        }
+      } else {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
+        const uint32_t* xw = &x.x;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 d = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(dw + w));
+          const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(xw + w));
+          acc += d.x * y.x + d.y * y.y;
+        }
+      }
+      return acc;
+    };
+    float d1 = dot(o), d2 = kDiff ? dot(o2) : 0.f;
+    const unsigned mask = __activemask();  // whole groups of kLanes lanes
+#pragma unroll
+    for (int s = kLanes / 2; s > 0; s >>= 1) {
+      d1 += __shfl_xor_sync(mask, d1, s);
+      if (kDiff) d2 += __shfl_xor_sync(mask, d2, s);
+    }
+    if (sub == 0) {
+      const size_t dst = size_t(bh) * g.S + pos;
+#pragma unroll
+      for (int m = 0; m < (kDiff ? 2 : 1); ++m) {
+        const float l = lse[m * all + row];
+        lse2[m * all + dst] = l == -INFINITY ? INFINITY : l * kLog2e;
+      }
+      dsum[dst] = kDiff ? fmaf(lm, d2, d1) : d1;  // out = O_1 - lambda O_2
+      if (kDiff) dsum[all + dst] = d2;
+    }
+  }
+}
+
+// One pass over a tile of 128 rows (two blocks of one head): kQ = true, the
+// query pass (rows are queries; Q and dO stay, K and V stream; -> dQ and D), or
+// the key pass (rows are keys; K and V stay, Q, dO and their row statistics
+// stream; -> dK, dV and the table's gradient). Rows are TMEM lanes in both:
+//   S_m = A1_m B1_m^T, dP = A2 B2^T      (A1, A2 the tile's, B1, B2 a block's)
+//   row warps: P_m and dS_m as bf16 over S and dP in TMEM
+//   Y_m += dS_m B1_m                     (dQ or dK)
+//   X  += Pc B2 (key pass: dV), X_m += P_m B1_m (query pass: P K)
+// A step is W columns of a streamed block (64 with one map, 32 with two), in one
+// of two TMEM stages; the row warps of group s work on stage s, so that one
+// group's loads, stores and waits lie beside the other's exponentials.
+// TMEM columns: X 0, Y 128, the stages at 256 and 384: S_1, (S_2,) dP, W each. A
+// row thread owns 16-column chunks: P_m goes into the first 8 columns of its own
+// chunk of S_m (key pass: Pc over S_1), dS_1 and dS_2 into the two halves of dP's,
+// so nobody overwrites what another warp has still to read.
+template <int D, AttnMode M, int L, bool kQ>
+__global__ void __launch_bounds__(kSbThreads, 1)
+    score_bwd_kernel(const __grid_constant__ ScoreBwdArgs a, const Geometry g) {
+  constexpr bool kDiff = M == AttnMode::kDiff, kTable = !kDiff && !kQ;
+  constexpr int NM = kDiff ? 2 : 1;
+  constexpr int W = kDiff ? 32 : 64, kHalves = 64 / W;  // columns of a step, steps of a block
+  constexpr uint32_t kColX = 0, kColY = 128, kStage0 = 256, kStage = 128, kDP = W * NM;
+  extern __shared__ uint8_t sb_raw[];
+  SbSmem<D>& sm = *reinterpret_cast<SbSmem<D>*>(
+      (reinterpret_cast<uintptr_t>(sb_raw) + 1023) & ~uintptr_t(1023));
+  SbBars& br = sm.bar;
+  float* bias = reinterpret_cast<float*>(&sm + 1);
+  const int noff = relbias_offsets(g);
+  float* hist = bias + noff;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = blockIdx.y;
+  // (query tiles heaviest first)
+  const int tile = kQ ? a.order[size_t(bh) * g.ntile + blockIdx.x] : int(blockIdx.x);
+  int ba, bb;  // the tile's blocks (bb = -1: a lone block)
+  tile_blocks(g, tile, ba, bb);
+  const size_t unit = size_t(bh) * g.ntile + tile;
+  const int nblk = kQ ? a.tcnt[unit] : a.kcnt[unit];
+  const int n = nblk * kHalves;
+  const int32_t* glist = (kQ ? a.tidx : a.kidx) + unit * g.nb;
+  for (int i = threadIdx.x; i < nblk && i < kSbList; i += kSbThreads) sm.list[i] = glist[i];
+  auto at = [&](int i) -> int { return i < kSbList ? sm.list[i] : __ldg(glist + i); };
+  if constexpr (!kDiff) relbias_load(bias, a.bias, g, bh, threadIdx.x, kSbThreads, a.status);
+  if constexpr (kTable)
+    for (int i = threadIdx.x; i < noff; i += kSbThreads) hist[i] = 0.f;
+  if (threadIdx.x == 0) {
+    br.abort = 0;
+    mbar_init(&br.tile_full, 1);
+    for (int s = 0; s < kSbSlots; ++s) {
+      mbar_init(&br.full[s], 2);
+      mbar_init(&br.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&br.s_full[s], 1);
+      mbar_init(&br.out_full[s], kSbRowWarps / 2);
+    }
+    mbar_init(&br.acc_full, 1);
+    mbar_init(&br.dsum_full, kSbRowWarps);
+    mbar_init(&br.drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&br.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, br.tmem_base, 0);
+  volatile int* abort = &br.abort;
+
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ producers
+    // warp 0: the tile, then B1 (and the row statistics); warp 2: B2
+    if (lane == 0 && nblk > 0) {
+      const CUtensorMap* map =
+          kQ ? (warp == 0 ? &a.map_k : &a.map_v) : (warp == 0 ? &a.map_q : &a.map_do);
+      prefetch_tensormap(map);
+      if (warp == 0) {
+        mbar_arrive_expect_tx(&br.tile_full, 2u * 128u * D * 2u);
+        for (int e = 0; e < 2; ++e) {
+          const int blk = (e == 0 || bb < 0) ? ba : bb;  // a lone block: its copy fills the rest
+          int t, hp, wp;
+          block_coords(g, blk, t, hp, wp);
+          for (int c = 0; c < D / 64; ++c) {
+            tma_load_5d(&sm.ta[c][e * kBlk], kQ ? &a.map_q : &a.map_k, &br.tile_full, c * 64,
+                        wp * g.pw, hp * g.ph, t * g.pt, bh);
+            tma_load_5d(&sm.tb[c][e * kBlk], kQ ? &a.map_do : &a.map_v, &br.tile_full, c * 64,
+                        wp * g.pw, hp * g.ph, t * g.pt, bh);
+          }
+        }
+      }
+      int last = -1;
+      for (int j = 0; j < nblk; ++j) {
+        const int s = j % kSbSlots;
+        if (j >= kSbSlots && !mbar_wait(&br.empty[s], (j / kSbSlots - 1) & 1, abort)) {
+          fail_s(a.status, &br.abort, kDevErrTimeoutLoad);
+          break;
+        }
+        if (*abort) break;
+        if (j == 0 && warp == 0 && (a.debug_flags & SA_DEBUG_STALL_LOADER)) continue;  // test hook
+        int blk = at(j) & kEntryBlockMask;
+        if (blk >= g.nb) {
+          atomicOr(a.status, kDevErrBadIndex);
+          blk = 0;
+        }
+        int t, hp, wp;
+        block_coords(g, blk, t, hp, wp);
+        mbar_arrive_expect_tx(&br.full[s],
+                              64u * D * 2u + (!kQ && warp == 0 ? uint32_t(NM) * 512u : 0u));
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_5d(warp == 0 ? &sm.sa[s][c][0] : &sm.sb[s][c][0], map, &br.full[s], c * 64,
+                      wp * g.pw, hp * g.ph, t * g.pt, bh);
+        if (!kQ && warp == 0) {
+          for (int m = 0; m < NM; ++m) {
+            const size_t off = (size_t(m) * g.BH + bh) * g.S + size_t(blk) * 64;
+            bulk_load(&sm.lse2[s][m][0], a.lse2 + off, 256u, &br.full[s]);
+            bulk_load(&sm.dsum[s][m][0], a.dsum + off, 256u, &br.full[s]);
+          }
+        }
+        last = j;
+      }
+      if (*abort) {
+        // let the copies land before the CTA can exit (time-bounded, ignoring
+        // the abort flag): at most the last use of each slot is open
+        int never = 0;
+        if (warp == 0) mbar_wait(&br.tile_full, 0, &never);
+        for (int jj = last; jj >= 0 && jj > last - kSbSlots; --jj)
+          mbar_wait(&br.full[jj % kSbSlots], (jj / kSbSlots) & 1, &never);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA
+    // The whole warp walks the steps, so that the loop's values are uniform (the
+    // descriptors stay in uniform registers); one elected lane issues.
+    if (nblk > 0) {
+      constexpr uint32_t id_s = idesc_bf16_f32(128, W, 0, 0);
+      constexpr uint32_t id_y = idesc_bf16_f32(128, kDiff ? 64 : D, 0, 1);
+      constexpr uint32_t id_x = kQ ? id_y : idesc_bf16_f32(128, D, 0, 1);
+      constexpr uint32_t kSlot = (D / 64) * kBlk / 16;   // a slot in descriptor units
+      constexpr uint32_t kHalf = W * 128 / 16;           // W rows of a block
+      constexpr uint32_t kMap = D == 128 ? kBlk / 16 : 0;  // a map's channels of a block
+      const uint64_t a1 = sw128_desc(smem_u32(&sm.ta[0][0]), 16, 1024);
+      const uint64_t a2 = sw128_desc(smem_u32(&sm.tb[0][0]), 16, 1024);
+      const uint64_t b1 = sw128_desc(smem_u32(&sm.sa[0][0][0]), 16, 1024);
+      const uint64_t b2 = sw128_desc(smem_u32(&sm.sb[0][0][0]), 16, 1024);
+      const uint64_t b1_mn = sw128_desc(smem_u32(&sm.sa[0][0][0]), kBlk, 1024);
+      const uint64_t b2_mn = sw128_desc(smem_u32(&sm.sb[0][0][0]), kBlk, 1024);
+      auto where = [&](int i) -> uint64_t {
+        return uint64_t((i / kHalves) % kSbSlots) * kSlot + uint64_t(i % kHalves) * kHalf;
+      };
+      const bool one = elect_one();
+      auto issue = [&](int i) {
+        const uint32_t st = tmem + kStage0 + kStage * uint32_t(i & 1);
+        if (!one) return;
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+          mma_scores<D / 16 / NM>(st + W * m, a1, kTile, b1 + where(i), kBlk, id_s,
+                                  m * (D / 16 / NM));
+        mma_scores<D / 16>(st + kDP, a2, kTile, b2 + where(i), kBlk, id_s, 0);
+        mma_commit(&br.s_full[i & 1]);
+      };
+      bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&br.tile_full, 0, abort) &&
+                                            mbar_wait(&br.full[0], 0, abort));
+      if (ok) {
+        tc_fence_after_sync();
+        issue(0);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        if (i + 1 < n) {
+          // stage (i + 1) & 1 was last read by step i - 1's products, issued before
+          const int j = (i + 1) / kHalves;
+          if ((i + 1) % kHalves == 0)
+            ok = __all_sync(0xFFFFFFFFu,
+                            mbar_wait(&br.full[j % kSbSlots], (j / kSbSlots) & 1, abort));
+          if (!ok) break;
+          tc_fence_after_sync();
+          issue(i + 1);
+        }
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&br.out_full[i & 1], (i >> 1) & 1, abort));
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t st = tmem + kStage0 + kStage * uint32_t(i & 1);
+        const uint32_t acc = i > 0 ? 1u : 0u;
+        if (one) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+          if (kQ)
+            mma_from_tmem<W / 16>(tmem + kColX + 64u * m, st + W * m, b1_mn + where(i) + m * kMap,
+                                  id_x, acc);
+          else if (m == 0)
+            mma_from_tmem<W / 16>(tmem + kColX, st, b2_mn + where(i), id_x, acc);
+          mma_from_tmem<W / 16>(tmem + kColY + 64u * m, st + kDP + 8u * m,
+                                b1_mn + where(i) + m * kMap, id_y, acc);
+        }
+        if ((i + 1) % kHalves == 0) mma_commit(&br.empty[(i / kHalves) % kSbSlots]);
+        }
+        __syncwarp();
+      }
+      if (ok) {
+        if (one) mma_commit(&br.acc_full);
+      } else {
+        fail_s(a.status, &br.abort, kDevErrTimeoutMma);
+        if (one) mma_commit(&br.drain);  // wait (bounded) for the MMAs issued before exit
+        int never = 0;
+        mbar_wait(&br.drain, 0, &never);
+      }
+    }
+  } else if (warp >= 4) {
+    // ----------------------------------------------------------------- rows
+    const int part = (warp - 4) >> 2;              // 0..3
+    const int grp = part >> 1, wg = part & 1;      // steps of parity grp, half wg of the columns
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;                // TMEM lane: a row of the tile
+    const uint32_t lane_base = tmem + (uint32_t(quad * 32) << 16);
+    const bool valid = r < 64 || bb >= 0;          // uniform across the warp
+    const int blk = r < 64 || bb < 0 ? ba : bb;
+    const int my_keep = !valid ? 0 : r < 64 ? kEntryKeepA : kEntryKeepB;
+    const float sl2 = a.scale_log2;
+    const float lam = kDiff ? __bfloat162float(a.lam[bh % a.H]) : 0.f;
+    const size_t my_pos = size_t(bh) * g.S + size_t(blk) * 64 + (r & 63);
+    float lse2[NM], dsum[NM], dfull[NM];  // query pass: this row's
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      lse2[m] = kQ ? a.lse2[size_t(m) * g.BH * g.S + my_pos] : 0.f;
+      dsum[m] = kQ ? a.dsum[size_t(m) * g.BH * g.S + my_pos] : 0.f;
+      dfull[m] = 0.f;
+    }
+    constexpr int kSign = kQ ? 1 : -1;
+    RelBiasRow rb;
+    if constexpr (!kDiff) rb = relbias_row(g, blk, r & 63, kSign);
+    const uint32_t st = lane_base + kStage0 + kStage * uint32_t(grp);
+    bool ok = true;
+    for (int i = grp; i < n; i += 2) {
+      const int j = i / kHalves, s = j % kSbSlots;
+      const int ent = at(j);
+      const bool keep = (ent & my_keep) != 0;  // uniform across the warp
+      ok = __all_sync(0xFFFFFFFFu,
+                      mbar_wait(&br.s_full[grp], (i >> 1) & 1, abort) &&
+                          (kQ || mbar_wait(&br.full[s], (j / kSbSlots) & 1, abort)));
+      if (!ok) break;
+      tc_fence_after_sync();
+      float f[Cols<L>::kF], c[Cols<L>::kG], gf[Cols<L>::kF], gc[Cols<L>::kG];
+      int it = 0, ih = 0, iw = 0;
+      if constexpr (!kDiff) {
+        if (keep) {
+          relbias_block(g, rb, ent & kEntryBlockMask, kSign, it, ih, iw);
+          load_bias32<L>(bias, g, it, ih, iw, wg, kSign, f, c);
+          if constexpr (kTable) {
+#pragma unroll
+            for (int x = 0; x < Cols<L>::kF; ++x) gf[x] = 0.f;
+#pragma unroll
+            for (int y = 0; y < Cols<L>::kG; ++y) gc[y] = 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int ch = 0; ch < W / 32; ++ch) {
+        const int col = (W / 2) * wg + 16 * ch;                       // in the stage
+        const int qcol = (kDiff ? 32 * (i % kHalves) : 0) + col;      // in the streamed block
+        uint32_t pk[NM][8], ds[NM][8];
+        if (keep) {
+          uint32_t x[NM][16], dp[16];
+#pragma unroll
+          for (int m = 0; m < NM; ++m) tmem_ld16(st + W * m + col, x[m]);
+          tmem_ld16(st + kDP + col, dp);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            float pp[NM][2], dd[NM][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float e = __uint_as_float(dp[k + u]);
+#pragma unroll
+              for (int m = 0; m < NM; ++m) {
+                const float ls = kQ ? lse2[m] : sm.lse2[s][m][qcol + k + u];
+                const float dm = kQ ? dsum[m] : sm.dsum[s][m][qcol + k + u];
+                float z;
+                if constexpr (kDiff) {
+                  z = fmaf(__uint_as_float(x[m][k + u]), sl2, -ls);
+                } else {
+                  const int q = 16 * ch + k + u;
+                  z = fmaf(__uint_as_float(x[m][k + u]), sl2,
+                           f[q / Cols<L>::kG] + (c[q % Cols<L>::kG] - ls));
+                }
+                const float p = ex2_approx(z);
+                if (kQ) dfull[m] = fmaf(p, e, dfull[m]);
+                const float w = m == 0 ? p : lam * p;
+                pp[m][u] = kQ ? p : w;
+                dd[m][u] = m == 0 ? w * (e - dm) : w * (dm - e);
+                if constexpr (kTable) {
+                  const int q = 16 * ch + k + u;
+                  gf[q / Cols<L>::kG] += dd[0][u];
+                  gc[q % Cols<L>::kG] += dd[0][u];
+                }
+              }
+            }
+            if constexpr (kDiff && !kQ) {
+              pk[0][k / 2] = pack_bf16x2(pp[0][0] - pp[NM - 1][0], pp[0][1] - pp[NM - 1][1]);
+            } else {
+#pragma unroll
+              for (int m = 0; m < NM; ++m) pk[m][k / 2] = pack_bf16x2(pp[m][0], pp[m][1]);
+            }
+#pragma unroll
+            for (int m = 0; m < NM; ++m) ds[m][k / 2] = pack_bf16x2(dd[m][0], dd[m][1]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int m = 0; m < NM; ++m) pk[m][k] = ds[m][k] = 0u;
+        }
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+          if (kQ || m == 0) tmem_st8(st + W * m + col, pk[m]);
+          tmem_st8(st + kDP + col + 8 * m, ds[m]);
+        }
+      }
+      tmem_wait_st();
+      warp_arrive(&br.out_full[grp], lane);
+      if constexpr (kTable) {
+        if (keep) add_table_grad<L>(hist, g, it, ih, iw, wg, lane, gf, gc);
+      }
+    }
+    if (kQ && ok) {
+      // D of every row: four warps' partial sums, in a fixed order
+      float* sums = &sm.lse2[0][0][0];  // [map][part][row]
+#pragma unroll
+      for (int m = 0; m < NM; ++m) sums[(m * 4 + part) * 128 + r] = dfull[m];
+      warp_arrive(&br.dsum_full, lane);
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&br.dsum_full, 0, abort));
+      if (ok) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+          const float* x = sums + m * 512 + r;
+          dfull[m] = (x[0] + x[128]) + (x[256] + x[384]);
+        }
+      }
+    }
+    if (!ok) {
+      fail_s(a.status, &br.abort, kDevErrTimeoutSoftmax);
+    } else if (valid) {  // uniform across the warp
+      if (kQ && part == 0) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m) a.dsum[size_t(m) * g.BH * g.S + my_pos] = dfull[m];
+      }
+      if (32 * part < D) {
+        if (n > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&br.acc_full, 0, abort))) {
+          fail_s(a.status, &br.abort, kDevErrTimeoutSoftmax);
+        } else {
+          if (n > 0) tc_fence_after_sync();
+          const int c = 32 * part;
+          const size_t dst = (size_t(bh) * g.S + block_row_token(g, blk, r & 63)) * D + c;
+          const uint32_t y = lane_base + kColY + acc_col<D, kDiff>(c);
+          if constexpr (kQ) {
+            const int m = kDiff && c >= D / 2 ? NM - 1 : 0;
+            float fix = dfull[m] - dsum[m];
+            if (kDiff && m > 0) fix *= -lam;  // dS_2 = -lambda P_2 (dP - D_2)
+            store_acc32(y, lane_base + kColX + acc_col<D, kDiff>(c), n > 0, a.scale, fix, a.dq, dst,
+                        a.out_fp32);
+          } else {
+            store_acc32(lane_base + kColX + c, 0u, n > 0, 1.f, 0.f, a.dv, dst, a.out_fp32);
+            store_acc32(y, 0u, n > 0, a.scale, 0.f, a.dk, dst, a.out_fp32);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+  if constexpr (kTable) {
+    float* dst = a.part + unit * noff;
+    for (int i = threadIdx.x; i < noff; i += kSbThreads) dst[i] = hist[i];
+  }
+}
+
+// dtable: per head, the tiles' partial sums over offsets (part [BH][ntile][noff])
+// added over batch and tiles in a fixed order, 32 offsets x 32 groups of tiles
+// at a time, then over the offsets of each bucket. One CTA per head.
+__global__ void __launch_bounds__(1024)
+    dtable_kernel(const float* __restrict__ part, BiasArgs b, int B, void* __restrict__ dtable,
+                  int fp32, Geometry g) {
+  __shared__ float sums[2 * kRelBiasMaxAxes], red[32][33];
+  const int h = blockIdx.x, lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int noff = relbias_offsets(g);
+  for (int o0 = 0; o0 < noff; o0 += 32) {
+    const int o = o0 + lane;
+    float s = 0.f;
+    if (o < noff) {
+      for (int e = 0; e < B; ++e) {
+        const float* src = part + (size_t(e) * b.H + h) * g.ntile * noff + o;
+#pragma unroll 4
+        for (int t = grp; t < g.ntile; t += 32) s += src[size_t(t) * noff];
+      }
+    }
+    red[grp][lane] = s;
+    __syncthreads();
+    float x = red[lane][grp];  // group `lane` of offset o0 + grp
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, k);
+    if (lane == 0 && o0 + grp < noff) sums[o0 + grp] = x;
+    __syncthreads();
+  }
+  for (int k = threadIdx.x; k < b.n_buckets; k += blockDim.x) {
+    float s = 0.f;
+    for (int i = 0; i < noff; ++i) {
+      int bk = __ldg(b.bucket + i);
+      if (bk < 0 || bk >= b.n_buckets) bk = 0;  // as the kernels read it
+      if (bk == k) s += sums[i];
+    }
+    const size_t at = size_t(h) * b.n_buckets + k;
+    if (fp32) static_cast<float*>(dtable)[at] = s;
+    else static_cast<__nv_bfloat16*>(dtable)[at] = __float2bfloat16_rn(s);
+  }
+}
+
+// dlambda[h] = -sum of D_2 (dsum's second map, [BH][S]) over the batch and the
+// rows, in a fixed order. One CTA per head.
+__global__ void __launch_bounds__(1024)
+    dlambda_kernel(const float* __restrict__ d2, int S, int B, int H, void* __restrict__ dlam,
+                   int fp32) {
+  __shared__ float red[32];
+  const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float s = 0.f;
+  for (int e = 0; e < B; ++e) {
+    const float4* src = reinterpret_cast<const float4*>(d2 + (size_t(e) * H + h) * S);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < S / 4; i += 1024) {
+      const float4 x = __ldg(src + i);
+      s += (x.x + x.y) + (x.z + x.w);
+    }
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
+  if (lane == 0) red[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    s = red[lane];
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
+    if (lane == 0) {
+      if (fp32) static_cast<float*>(dlam)[h] = -s;
+      else static_cast<__nv_bfloat16*>(dlam)[h] = __float2bfloat16_rn(-s);
+    }
+  }
+}
+
+template <int D, AttnMode M, int L, bool kQ>
+static cudaError_t launch_pass(const ScoreBwdArgs& a, const Geometry& g, cudaStream_t stream) {
+  // the offset tables, and in the key pass the histogram behind them; at least
+  // 120 KB, since each CTA allocates all 512 TMEM columns
+  const size_t tables =
+      M == AttnMode::kDiff ? 0 : (kQ ? 1 : 2) * relbias_offsets(g) * sizeof(float);
+  const size_t need = sizeof(SbSmem<D>) + 1024 + tables;
+  const int smem = int(need > 120 * 1024 ? need : 120 * 1024);
+  cudaError_t e = cudaFuncSetAttribute(score_bwd_kernel<D, M, L, kQ>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  score_bwd_kernel<D, M, L, kQ>
+      <<<dim3(unsigned(g.ntile), unsigned(g.BH)), kSbThreads, smem, stream>>>(a, g);
+  return cudaGetLastError();
+}
+
+template <int D, AttnMode M, int L>
+static cudaError_t launch_passes(const ScoreBwdArgs& a, const Geometry& g, cudaStream_t stream) {
+  const cudaError_t e = launch_pass<D, M, L, true>(a, g, stream);  // first: it corrects D
+  return e != cudaSuccess ? e : launch_pass<D, M, L, false>(a, g, stream);
+}
+
+template <int D>
+static cudaError_t launch_score_bwd_d(const ScoreBwdArgs& a, const Geometry& g,
+                                      cudaStream_t stream) {
+  if (a.lam != nullptr) return launch_passes<D, AttnMode::kDiff, 0>(a, g, stream);
+  switch (g.lpw < 5 ? g.lpw : 5) {  // columns of a block that are one run of w
+    case 0: return launch_passes<D, AttnMode::kBias, 0>(a, g, stream);
+    case 1: return launch_passes<D, AttnMode::kBias, 1>(a, g, stream);
+    case 2: return launch_passes<D, AttnMode::kBias, 2>(a, g, stream);
+    case 3: return launch_passes<D, AttnMode::kBias, 3>(a, g, stream);
+    case 4: return launch_passes<D, AttnMode::kBias, 4>(a, g, stream);
+    default: return launch_passes<D, AttnMode::kBias, 5>(a, g, stream);
+  }
+}
+
+cudaError_t launch_score_bwd(const ScoreBwdArgs& a, const Geometry& g, cudaStream_t stream) {
+  const dim3 grid(unsigned((g.S + kPrepRows - 1) / kPrepRows), unsigned(g.BH));
+  const bool diff = a.lam != nullptr;
+#define SA_PREP(D, DIFF)                                                                       \
+  score_prep_kernel<D, DIFF><<<grid, 256, 0, stream>>>(a.out, a.out2, a.dout, a.lse, a.lam, a.H, \
+                                                       a.lse2, a.dsum, a.out_fp32, g)
+  if (g.d == 128) {
+    if (diff) SA_PREP(128, true); else SA_PREP(128, false);
+  } else {
+    if (diff) SA_PREP(64, true); else SA_PREP(64, false);
+  }
+#undef SA_PREP
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_bwd_lists(a.bits, a.kcnt, a.kidx, g, stream);
+  if (e == cudaSuccess)
+    e = g.d == 128 ? launch_score_bwd_d<128>(a, g, stream) : launch_score_bwd_d<64>(a, g, stream);
+  if (e != cudaSuccess) return e;
+  if (diff)
+    dlambda_kernel<<<unsigned(a.H), 1024, 0, stream>>>(a.dsum + size_t(g.BH) * g.S, g.S,
+                                                       g.BH / a.H, a.H, a.dparam, a.out_fp32);
+  else
+    dtable_kernel<<<unsigned(a.H), 1024, 0, stream>>>(a.part, a.bias, g.BH / a.H, a.dparam,
+                                                      a.out_fp32, g);
+  return cudaGetLastError();
+}
+
+}  // namespace sa

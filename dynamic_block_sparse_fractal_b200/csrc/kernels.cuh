@@ -2,6 +2,7 @@
 // launch's cudaError_t; argument validation happens before any of them.
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -62,9 +63,33 @@ cudaError_t launch_radius(const RadiusArgs& a, const Geometry& g, cudaStream_t s
 // The radius kernel's limits: T <= 4096 frames, Hh, Ww <= 1024, nb <= 6144 blocks.
 bool radius_supported(const Geometry& g);
 
+// The caller's block mask (bytes, 0 = dropped; [BH][nb][nb], or one [nb][nb]
+// for all heads when head_stride is 0) as bitmaps, counts and ascending lists.
+cudaError_t launch_mask_rows(const uint8_t* mask, size_t head_stride, uint32_t* bits, int32_t* cnt,
+                             int32_t* idx, const Geometry& g, cudaStream_t stream);
+
 // Per head: tiles sorted by descending union length (ties by tile index).
 cudaError_t launch_tile_order(const int32_t* tcnt, int32_t* order, const Geometry& g,
                               cudaStream_t stream);
+
+// Score functions of the attention kernel: q.k alone, with a relative position
+// bias (kBias8: blocks whose rows are 8 tokens, pw == 8, the patch among them;
+// kBias: any block shape), or the two maps of differential attention.
+enum class AttnMode { kPlain, kBias, kBias8, kDiff };
+
+// Learned relative position bias: row bh % H of table [H][n_buckets] (bf16), read
+// through bucket[], the table index of every offset along t, then h, then w
+// ((2T-1) + (2Hh-1) + (2Ww-1) entries, offset key - query, lowest first).
+// Offsets along the three axes, and the most that the kernels' shared memory
+// holds (T + Hh + Ww <= 1152).
+SA_HD int relbias_offsets(const Geometry& g) { return 2 * (g.T + g.Hh + g.Ww) - 3; }
+constexpr int kRelBiasMaxAxes = 1152;
+struct BiasArgs {
+  const __nv_bfloat16* table;  // null: no bias
+  const int32_t* bucket;
+  int n_buckets;
+  int H;
+};
 
 struct AttnArgs {
   CUtensorMap map_q, map_k, map_v;  // 5-D patch maps, see tma_host.h
@@ -78,6 +103,11 @@ struct AttnArgs {
   int out_fp32;
   int debug_flags;
   float* lse;  // [BH][S] natural order: each row's log-sum-exp (natural log), or null
+               // (differential: [2][BH][S], one per map)
+  BiasArgs bias;             // relative position bias, or a null table
+  const __nv_bfloat16* lam;  // differential: [H] weights of the second map, or null
+  void* out2;                // differential: P_2 V [BH][S][d] like out, or null
+  int H;                     // differential: heads (bh % H picks lam's entry)
 };
 cudaError_t launch_attn(const AttnArgs& a, const Geometry& g, cudaStream_t stream);
 
@@ -143,6 +173,53 @@ cudaError_t launch_bwd(const BwdArgs& a, const Geometry& g, cudaStream_t stream)
 // dq = dq_acc (bf16 or fp32).
 cudaError_t launch_dq_convert(const float* dq_acc, void* dq, int out_fp32, const Geometry& g,
                               cudaStream_t stream);
+
+// Gradients with a relative position bias (lam null) or of differential
+// attention (lam given). Scratch regions as in ScoreBwdLayout.
+struct ScoreBwdArgs {
+  CUtensorMap map_q, map_k, map_v, map_do;  // 5-D patch maps, one block per box
+  const void* out;                          // the forward's output, P_2 v (diff), dout, lse
+  const void* out2;
+  const __nv_bfloat16* dout;
+  const float* lse;
+  float* lse2;  // [maps][BH][S] fractal order, log2 units
+  float* dsum;  // [maps][BH][S] fractal order: rowsum(dO * P_m V)
+  float* part;  // bias: [BH][ntile][offsets]
+  int32_t* kcnt;
+  int32_t* kidx;
+  const uint32_t* bits;
+  const int32_t* tcnt;
+  const int32_t* tidx;
+  const int32_t* order;
+  void* dq;  // [BH][S][d] natural order, bf16 or fp32
+  void* dk;
+  void* dv;
+  void* dparam;  // dtable [H][n_buckets] or dlambda [H]
+  BiasArgs bias;
+  const __nv_bfloat16* lam;
+  int H;
+  uint32_t* status;
+  float scale_log2;  // log2(e) * scale
+  float scale;       // 1 / sqrt(channels of a map)
+  int out_fp32;
+  int debug_flags;  // SA_DEBUG_STALL_LOADER: the first Q load is never issued (test hook)
+};
+cudaError_t launch_score_bwd(const ScoreBwdArgs& a, const Geometry& g, cudaStream_t stream);
+
+struct ScoreBwdLayout {
+  size_t lse2, dsum, kcnt, kidx, part, total;
+};
+inline ScoreBwdLayout make_score_bwd_layout(const Geometry& g, int maps, size_t parts_per_head) {
+  ScoreBwdLayout b;
+  size_t o = 0;
+  b.lse2 = o; o = align256(o + sizeof(float) * maps * size_t(g.BH) * g.S);
+  b.dsum = o; o = align256(o + sizeof(float) * maps * size_t(g.BH) * g.S);
+  b.kcnt = o; o = align256(o + sizeof(int32_t) * size_t(g.BH) * g.ntile);
+  b.kidx = o; o = align256(o + sizeof(int32_t) * size_t(g.BH) * g.ntile * g.nb);
+  b.part = o; o = align256(o + sizeof(float) * size_t(g.BH) * parts_per_head);
+  b.total = o;
+  return b;
+}
 
 constexpr int kHeatCtas = 148;  // one per SM of a B200
 inline int heat_ctas(const Geometry& g) {

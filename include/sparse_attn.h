@@ -15,7 +15,11 @@
  * them: the gradients over the same mask (sparse_attn_fwd_lse,
  * sparse_attn_bwd), the exact block max-pooled attention map that measures a
  * mask's recall (sparse_attn_block_heatmap), per-head block shapes (*_heads),
- * and the whole path as one CUDA graph launch (sparse_attn_graph_*).
+ * and the whole path as one CUDA graph launch (sparse_attn_graph_*). A plan can
+ * also come from the caller's own block mask (sparse_attn_plan_mask), and two
+ * other score functions run over any plan, each with its gradients: a learned
+ * relative position bias (sparse_attn_{fwd,bwd}_bias) and differential
+ * attention (sparse_attn_{fwd,bwd}_diff).
  *
  * Conventions for every entry point:
  *   - All tensor pointers are DEVICE pointers owned by the caller; the library
@@ -420,6 +424,98 @@ typedef struct sa_radius {
 sa_status sparse_attn_plan_radius(const sa_desc* desc, const sa_radius* radius,
                                   const float* entropy, void* workspace, size_t ws_bytes,
                                   void* stream);
+
+/* ---- A plan from the caller's own block mask -----------------------------
+ * (No counterpart on the pages: for masks from a learned scorer, from another
+ * step or from a layout the caller knows, padding among it.) Writes the
+ * per-q-block lists, the per-tile union lists and the tile order into
+ * `workspace` exactly as sparse_attn_plan does (desc->thr and the STA window
+ * are not used; the pooled means and logits are not written), so that every
+ * call that reads a plan runs on it. mask: device bytes, 0 = dropped, any other
+ * value = kept, blocks in fractal order, [B*H][nb][nb] (mask_heads = B*H), or
+ * one [nb][nb] for all heads (mask_heads = 1); no alignment needed. A q-block
+ * may keep nothing: its output rows are 0, their log-sum-exp -inf, and they
+ * give no gradient. SA_ERR_INVALID_ARG for any other mask_heads. */
+sa_status sparse_attn_plan_mask(const sa_desc* desc, const uint8_t* mask, int mask_heads,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- Learned relative position bias ---------------------------------------
+ * Attention over the planned blocks with a learned bias on each score:
+ *   z_ij = q_i . k_j / sqrt(d) + b_t[t_j - t_i] + b_h[h_j - h_i] + b_w[w_j - w_i]
+ * where (t, h, w) are a token's frame, row and column and each b_* reads the
+ * head's row of a table through a map from offsets to buckets. */
+typedef struct sa_rel_bias {
+  const void* table;     /* device bf16 [H][n_buckets], 2-byte aligned, in nats:
+                            row h serves head h of every batch entry. An entry at
+                            or below -1e30 (the type's lowest value, -inf) masks
+                            its offsets; other entries must be finite */
+  const int32_t* bucket; /* device int32, 4-byte aligned: the table index of every
+                            offset key - query, lowest first: the 2T-1 along t, then
+                            the 2Hh-1 along h, then the 2Ww-1 along w. Axes may
+                            share buckets. An index outside [0, n_buckets) reads
+                            entry 0 and is reported by sparse_attn_check */
+  int n_buckets;         /* 1 .. 4096 */
+} sa_rel_bias;
+
+/* sparse_attn_fwd with the bias. lse (may be NULL): as for sparse_attn_fwd_lse,
+ * of the biased scores. The workspace holds any plan made for the same desc.
+ * SA_ERR_UNSUPPORTED when T + Hh + Ww > 1152. A row whose kept offsets are all
+ * masked is treated as one that keeps nothing. */
+sa_status sparse_attn_fwd_bias(const sa_desc* desc, const sa_rel_bias* bias, const void* q,
+                               const void* k, const void* v, const void* workspace,
+                               size_t ws_bytes, void* out, float* lse, void* stream);
+
+/* Bytes of device scratch sparse_attn_bwd_bias needs: two fp32 [B*H][S] row
+ * statistics, the transposed block lists, and one partial sum per query tile
+ * and offset. */
+sa_status sparse_attn_bwd_bias_scratch_size(const sa_desc* desc, size_t* bytes);
+
+/* Gradients of sum(out * dout): dq, dk, dv as for sparse_attn_bwd with P of the
+ * biased scores, and dtable [H][n_buckets] (bf16, fp32 if desc->out_fp32,
+ * 4-byte aligned, overwritten): the sum of dS = P (dP - D) over the batch and
+ * over every kept pair whose offset along an axis falls into the bucket, axis
+ * by axis. dq, dk and dv are the same bits at every run of the same inputs;
+ * dtable's sums of one query tile are fp32 additions in no fixed order. out,
+ * lse: what sparse_attn_fwd_bias wrote. Scratch as for sparse_attn_bwd, of
+ * sparse_attn_bwd_bias_scratch_size() bytes. */
+sa_status sparse_attn_bwd_bias(const sa_desc* desc, const sa_rel_bias* bias, const void* q,
+                               const void* k, const void* v, const void* out, const void* dout,
+                               const float* lse, const void* workspace, size_t ws_bytes, void* dq,
+                               void* dk, void* dv, void* dtable, void* scratch,
+                               size_t scratch_bytes, void* stream);
+
+/* ---- Differential attention -------------------------------------------------
+ * The difference of two softmax maps over the planned blocks, with e = d/2 and
+ * q = [q1, q2], k = [k1, k2] split along the channels:
+ *   P_m = softmax(q_m k_m^T / sqrt(e)),   out = (P_1 - lambda_h P_2) v
+ * lambda: device bf16 [H], 2-byte aligned: the weight of each head's second
+ * map, as the caller's parametrisation gives it (the norm of the heads that a
+ * model may put behind it is the caller's). d = 64 or 128 as for the other
+ * calls: the maps have 32 or 64 channels, v all d. */
+
+/* out2 (may be NULL): P_2 v, [B,H,S,d] in out's type; lse (may be NULL): fp32
+ * [2][B*H][S], the log-sum-exp of each map's rows. Both are what
+ * sparse_attn_bwd_diff reads. The workspace holds any plan made for the desc. */
+sa_status sparse_attn_fwd_diff(const sa_desc* desc, const void* lambda, const void* q,
+                               const void* k, const void* v, const void* workspace,
+                               size_t ws_bytes, void* out, void* out2, float* lse, void* stream);
+
+/* Bytes of device scratch sparse_attn_bwd_diff needs: four fp32 [B*H][S] row
+ * statistics, the transposed block lists and partial sums of dlambda. */
+sa_status sparse_attn_bwd_diff_scratch_size(const sa_desc* desc, size_t* bytes);
+
+/* Gradients of sum(out * dout): dq, dk, dv [B,H,S,d] and dlambda [H] (bf16,
+ * fp32 if desc->out_fp32, 4-byte aligned), all overwritten, the same bits at
+ * every run of the same inputs. With dP = dout v^T and D_m = rowsum(dout *
+ * P_m v): dv = (P_1 - lambda P_2)^T dout, dS_1 = P_1 (dP - D_1), dS_2 = -lambda
+ * P_2 (dP - D_2), dq_m = dS_m k_m / sqrt(e), dk_m = dS_m^T q_m / sqrt(e),
+ * dlambda = -sum D_2 over the batch and the rows. out, out2, lse: what
+ * sparse_attn_fwd_diff wrote. */
+sa_status sparse_attn_bwd_diff(const sa_desc* desc, const void* lambda, const void* q,
+                               const void* k, const void* v, const void* out, const void* out2,
+                               const void* dout, const float* lse, const void* workspace,
+                               size_t ws_bytes, void* dq, void* dk, void* dv, void* dlambda,
+                               void* scratch, size_t scratch_bytes, void* stream);
 
 #ifdef __cplusplus
 }
