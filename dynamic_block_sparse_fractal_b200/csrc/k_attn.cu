@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = sm.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm.tmem_base, 0);
 
   // Warpgroup 0 (three producers and the MMA issuer) gives registers to the
   // softmax warpgroups: 128 x 72 + 256 x 216 = 384 x 168, the launch's
@@ -380,8 +380,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warps, so the bookkeeping between MMA batches is kept to a minimum
     // (each instruction here idles the tensor core once its short queue
     // drains), and each op's MMAs go out from one asm block with no compiler
-    // instructions between them (3-4 % faster than one asm per MMA).
-    if (lane == 0) {
+    // instructions between them (3-4 % faster than one asm per MMA). The whole
+    // warp walks the steps and one elected lane issues: the loop's values are
+    // then uniform across the warp and the operands of an MMA need no moves from
+    // the lane's own registers.
+    {
+      const bool one = elect_one();
       const uint32_t id_s2 = idesc_bf16_f32(128, 128, 0, 0);
       const uint32_t id_s1 = idesc_bf16_f32(128, 64, 0, 0);
       const uint32_t id_pv = idesc_bf16_f32(128, D, 0, 1);
@@ -392,16 +396,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t qdesc0 = sw128_desc(smem_u32(&sm.q[0][0][0]), 16, 1024);
       const uint64_t qdesc1 = sw128_desc(smem_u32(&sm.q[1][0][0]), 16, 1024);
       constexpr uint32_t kSlotStep = (D / 64) * kChunkBytes / 16;  // one slot, 16 B units
-      const int n0 = tile[0].nsteps, n1 = tile[1].nsteps;
-      const int u0 = tile[0].n_u, u1 = tile[1].n_u;
+      const int u0 = __shfl_sync(0xFFFFFFFFu, tile[0].n_u, 0);
+      const int u1 = __shfl_sync(0xFFFFFFFFu, tile[1].n_u, 0);
+      const int n0 = (u0 + 1) >> 1, n1 = (u1 + 1) >> 1;
       bool ok = n0 == 0 || mbar_wait(&sm.q_full[0], 0, abort);  // (heaviest first: n1 <= n0)
       if (!kDiff && ok && n1 > 0) ok = mbar_wait(&sm.q_full[1], 0, abort);
+      ok = __all_sync(0xFFFFFFFFu, ok);
       int k = 0;  // op index (ring position)
 #if SA_TRACE
       int tr_u = 0;
 #endif
       // S_X(step) = Q_X K^T into tile X's S columns, the K pair in slot s
       auto mma_s = [&](int x, int step, int s) {
+        if (!one) return;
         const uint64_t qd = x ? qdesc1 : qdesc0;
         const uint64_t kd = kdesc0 + uint64_t(s) * kSlotStep;
         const uint32_t id = ((x ? u1 : u0) - 2 * step) >= 2 ? id_s2 : id_s1;
@@ -426,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // O_X += P_X V, P from tile X's S columns in TMEM, the V pair in slot s
       auto mma_pv = [&](int x, int step, int s) {
+        if (!one) return;
         const uint64_t vd = vdesc0 + uint64_t(s) * kSlotStep;
         const uint32_t o_tmem = tmem + col_o(x);
         const uint32_t p_tmem = tmem + col_s(x);
@@ -439,10 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < 2; ++x) {
         if (!ok || (x ? n1 : n0) == 0) continue;
         const int s = k & (kSlots - 1);
-        ok = mbar_wait(&sm.full[s], (k / kSlots) & 1, abort);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[s], (k / kSlots) & 1, abort));
         if (!ok) break;
         mma_s(x, 0, s);
-        mma_commit(&sm.empty[s]);  // also tells the softmax that S_X(0) is complete
+        if (one) mma_commit(&sm.empty[s]);  // also tells the softmax that S_X(0) is complete
         ++k;
       }
       // One unit per tile and step: PV_X(j) and S_X(j+1) issued back to back
@@ -465,10 +473,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ready = mbar_peek3(&sm.p_full[x], j & 1, &sm.full[s_pv], par_pv,
                                             has_s ? &sm.full[s_s] : &sm.full[s_pv],
                                             has_s ? par_s : par_pv);
-          if (ready != 7u) {
+          if (!__all_sync(0xFFFFFFFFu, ready == 7u)) {
             ok = ((ready & 1u) || mbar_wait(&sm.p_full[x], j & 1, abort)) &&
                  ((ready & 2u) || mbar_wait(&sm.full[s_pv], par_pv, abort)) &&
                  ((ready & 4u) || !has_s || mbar_wait(&sm.full[s_s], par_s, abort));
+            ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
           }
 #if SA_TRACE
@@ -476,17 +485,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #endif
           tc_fence_after_sync();  // P was written by the softmax threads
           mma_pv(x, j, s_pv);
-          mma_commit(&sm.empty[s_pv]);
+          if (one) mma_commit(&sm.empty[s_pv]);
           if (has_s) {
             mma_s(x, j + 1, s_s);
-            mma_commit(&sm.empty[s_s]);  // also tells the softmax that S_X(j+1) is complete
+            if (one) mma_commit(&sm.empty[s_s]);  // also tells the softmax that S_X(j+1) is complete
             k += 2;
           } else {
-            mma_commit(&sm.o_final[x]);
+            if (one) mma_commit(&sm.o_final[x]);
             k += 1;
           }
 #if SA_TRACE
-          if (tr && tr_u < kTraceUnits) {
+          if (tr && one && tr_u < kTraceUnits) {
             g_attn_trace[3 * tr_u] = tr_t0;
             g_attn_trace[3 * tr_u + 1] = tr_t1;
             g_attn_trace[3 * tr_u + 2] = clock64();
@@ -497,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         fail(a.status, &sm.abort, kDevErrTimeoutMma);
-        mma_commit(&sm.drain);  // wait for this thread's in-flight MMAs
+        if (one) mma_commit(&sm.drain);  // wait for the in-flight MMAs
         int never = 0;
         mbar_wait(&sm.drain, 0, &never);
       }
