@@ -497,8 +497,8 @@ static sa_status score_bwd_impl(const sa_desc* desc, const BiasArgs& bias, const
   a.out2 = out2;
   a.dout = static_cast<const __nv_bfloat16*>(dout);
   a.lse = lse;
-  a.lse2 = at<float>(scratch, b.lse2);
-  a.dsum = at<float>(scratch, b.dsum);
+  a.nlse = at<float>(scratch, b.nlse);
+  a.ndsum = at<float>(scratch, b.ndsum);
   a.part = at<float>(scratch, b.part);
   a.kcnt = at<int32_t>(scratch, b.kcnt);
   a.kidx = at<int32_t>(scratch, b.kidx);

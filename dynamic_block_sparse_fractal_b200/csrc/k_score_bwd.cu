@@ -28,6 +28,7 @@
 #include <cuda_runtime.h>
 
 #include "kernels.cuh"
+#include "exp2_poly.cuh"
 #include "relbias.cuh"
 #include "sm100.cuh"
 
@@ -39,7 +40,7 @@ constexpr int kSbThreads = 640;   // warps 0, 2 TMA, 1 MMA, 3 idle; 4-19 rows
 constexpr int kSbRowWarps = 16;   // two groups of 8: the even and the odd steps; in a group two
                                   // warpgroups of 128 rows, half of a step's columns each
 constexpr int kSbList = 2880;     // list entries staged in shared memory (the rest from L2)
-constexpr int kSbSlots = 4;       // ring of streamed blocks
+constexpr int kSbSlots = 4;       // ring of streamed blocks (3 in the key pass with a table)
 constexpr int kTile = 128 * 128;  // 128 rows x 128 B (64 bf16 channels)
 constexpr int kBlk = 64 * 128;    // 64 rows x 128 B
 constexpr float kLog2e = 1.4426950408889634f;
@@ -205,11 +206,13 @@ __device__ __forceinline__ int lane_sums(float (&v)[N], int lane, int& first, bo
 }
 
 // dS of this thread's key against 32 query columns of a block, already summed
-// over each run (f) and each column (c), added to the CTA's histogram over
-// offsets (the layout of the bias tables; t, h, w: the block's indexes). Lanes of
-// a warp are 32 tokens of one block: their low L bits are the column. Sums over
-// the lanes that share an address come first, so that a warp issues a few
-// additions with few conflicts.
+// over each run (f) and each column (c), added to the warp's own histogram over
+// offsets (t, h, w: the block's indexes in it). Lanes of a warp are 32 tokens of
+// one block: their low L bits are the column. Lanes that share an address sum
+// first; then one group of lanes at a time adds, whose addresses all differ, so
+// that no atomics are needed (histograms shared by the CTA's warps with atomic
+// additions took 4,500 cycles a step, three times the step's products). Blocks
+// of several frames can still meet at an address and add atomically.
 template <int L>
 __device__ __forceinline__ void add_table_grad(float* hist, const Geometry& g, int t, int h, int w,
                                                int wg, int lane, float (&f)[Cols<L>::kF],
@@ -221,28 +224,62 @@ __device__ __forceinline__ void add_table_grad(float* hist, const Geometry& g, i
     for (int x = 0; x < NF; ++x) s += f[x];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if (lane == 0) atomicAdd(hist + t, s);
+    if (lane == 0) hist[t] += s;
   }
   int first;
   bool writer;
   int n = lane_sums<NF, 0, L>(f, lane, first, writer);  // lanes of one row run
-  if (writer) {
+  if (g.pt == 1) {
+    // lanes of equal column bits are different rows of the block
+    for (int q = 0; q < 1 << L; ++q) {
+      if (writer && (lane & ((1 << L) - 1)) == q) {
+#pragma unroll
+        for (int k = 0; k < NF; ++k)
+          if (k < n) hist[h - (f_run<L>(g, wg, first + k) & (g.ph - 1))] += f[k];
+      }
+      __syncwarp();
+    }
+  } else if (writer) {
 #pragma unroll
     for (int k = 0; k < NF; ++k) {
       if (k >= n) break;
       const int run = f_run<L>(g, wg, first + k);
-      if (g.pt != 1) atomicAdd(hist + t - (run >> g.lph), f[k]);
+      atomicAdd(hist + t - (run >> g.lph), f[k]);
       atomicAdd(hist + h - (run & (g.ph - 1)), f[k]);
     }
   }
+  __syncwarp();
   n = lane_sums<NG, L, 5>(c, lane, first, writer);  // lanes of one column
-  if (writer) {
 #pragma unroll
-    for (int k = 0; k < NG; ++k) {
-      if (k >= n) break;
-      atomicAdd(hist + w - g_col<L>(g, wg, first + k), c[k]);
+  for (int q = 0; q < 32 >> L; ++q) {  // lanes of one row run: different columns
+    if (writer && (lane >> L) == q) {
+#pragma unroll
+      for (int k = 0; k < NG; ++k)
+        if (k < n) hist[w - g_col<L>(g, wg, first + k)] += c[k];
     }
+    __syncwarp();
   }
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t f2_bf16(uint64_t a) {
+  float lo, hi;
+  f2_unpack(a, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ uint64_t f2_ex2(uint64_t a) {
+  float lo, hi;
+  f2_unpack(a, lo, hi);
+  return f2_pack(ex2_approx(lo), ex2_approx(hi));
+}
+__device__ __forceinline__ float f2_sum(uint64_t a) {
+  float lo, hi;
+  f2_unpack(a, lo, hi);
+  return lo + hi;
 }
 
 // What a CTA of either pass streams and waits on.
@@ -253,23 +290,32 @@ struct SbBars {
   int abort;
 };
 
-template <int D>
+template <int D, int kSlots>
 struct __align__(1024) SbSmem {
   uint8_t ta[D / 64][kTile], tb[D / 64][kTile];               // the tile's K, V (or Q, dO)
-  uint8_t sa[kSbSlots][D / 64][kBlk], sb[kSbSlots][D / 64][kBlk];  // streamed Q, dO (or K, V)
-  float lse2[kSbSlots][2][64], dsum[kSbSlots][2][64];         // of streamed query rows, per map
+  uint8_t sa[kSlots][D / 64][kBlk], sb[kSlots][D / 64][kBlk];  // streamed Q, dO (or K, V)
+  float nlse[kSbSlots][2][64], ndsum[kSbSlots][2][64];        // of streamed query rows, per map
   int32_t list[kSbList];
   SbBars bar;
 };
 // (the query pass sums each row's D over four warps in the statistics' place)
-// with the offset tables and the histogram of the largest grid, a CTA's 227 KB
-static_assert(sizeof(SbSmem<128>) + 1024 + 2 * sizeof(float) * (2 * kRelBiasMaxAxes - 3) <= 232448,
-              "shared memory of the gradient passes");
+// Floats of one row warp's histogram: the offsets between a token of one block
+// and any token, per axis.
+SA_HD int hist_floats(const Geometry& g) {
+  return (g.T + g.pt - 1) + (g.Hh + g.ph - 1) + (g.Ww + g.pw - 1);
+}
+// with the offset tables and the 16 histograms of the largest grid (pt + ph + pw
+// <= 66), a CTA's 227 KB
+static_assert(sizeof(SbSmem<128, 3>) + 1024 + sizeof(float) * (2 * kRelBiasMaxAxes - 3) +
+                      16 * sizeof(float) * (kRelBiasMaxAxes + 63) <= 232448,
+              "shared memory of the key pass");
+static_assert(sizeof(SbSmem<128, 4>) + 1024 + sizeof(float) * (2 * kRelBiasMaxAxes - 3) <= 232448,
+              "shared memory of the query pass");
 
 }  // namespace
 
-// D_m and lse_m * log2(e) of every row into fractal order (an empty row's
-// lse = -inf becomes +inf, so that 2^(z - lse) is 0). D/8 lanes per row, 128 rows
+// -D_m and -lse_m * log2(e) of every row into fractal order (negated: both are
+// addends; an empty row's lse = -inf stays -inf, so that 2^(z - lse) is 0). D/8 lanes per row, 128 rows
 // per CTA, one head per CTA.
 constexpr int kPrepRows = 128;
 
@@ -277,8 +323,8 @@ template <int D, bool kDiff>
 __global__ void __launch_bounds__(256)
     score_prep_kernel(const void* __restrict__ o, const void* __restrict__ o2,
                       const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse,
-                      const __nv_bfloat16* __restrict__ lam, int H, float* __restrict__ lse2,
-                      float* __restrict__ dsum, int fp32, Geometry g) {
+                      const __nv_bfloat16* __restrict__ lam, int H, float* __restrict__ nlse,
+                      float* __restrict__ ndsum, int fp32, Geometry g) {
   constexpr int kLanes = D / 8;
   const int sub = threadIdx.x % kLanes, bh = blockIdx.y;
   const size_t all = size_t(g.BH) * g.S;
@@ -325,10 +371,10 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int m = 0; m < (kDiff ? 2 : 1); ++m) {
         const float l = lse[m * all + row];
-        lse2[m * all + dst] = l == -INFINITY ? INFINITY : l * kLog2e;
+        nlse[m * all + dst] = l == -INFINITY ? l : -l * kLog2e;
       }
-      dsum[dst] = kDiff ? fmaf(lm, d2, d1) : d1;  // out = O_1 - lambda O_2
-      if (kDiff) dsum[all + dst] = d2;
+      ndsum[dst] = kDiff ? -fmaf(lm, d2, d1) : -d1;  // out = O_1 - lambda O_2
+      if (kDiff) ndsum[all + dst] = -d2;
     }
   }
 }
@@ -354,9 +400,11 @@ __global__ void __launch_bounds__(kSbThreads, 1)
   constexpr bool kDiff = M == AttnMode::kDiff, kTable = !kDiff && !kQ;
   constexpr int NM = kDiff ? 2 : 1;
   constexpr int W = kDiff ? 32 : 64, kHalves = 64 / W;  // columns of a step, steps of a block
+  constexpr int kSlots = kTable ? 3 : kSbSlots;
+  using Smem = SbSmem<D, kSlots>;
   constexpr uint32_t kColX = 0, kColY = 128, kStage0 = 256, kStage = 128, kDP = W * NM;
   extern __shared__ uint8_t sb_raw[];
-  SbSmem<D>& sm = *reinterpret_cast<SbSmem<D>*>(
+  Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(sb_raw) + 1023) & ~uintptr_t(1023));
   SbBars& br = sm.bar;
   float* bias = reinterpret_cast<float*>(&sm + 1);
@@ -376,11 +424,11 @@ __global__ void __launch_bounds__(kSbThreads, 1)
   auto at = [&](int i) -> int { return i < kSbList ? sm.list[i] : __ldg(glist + i); };
   if constexpr (!kDiff) relbias_load(bias, a.bias, g, bh, threadIdx.x, kSbThreads, a.status);
   if constexpr (kTable)
-    for (int i = threadIdx.x; i < noff; i += kSbThreads) hist[i] = 0.f;
+    for (int i = threadIdx.x; i < kSbRowWarps * hist_floats(g); i += kSbThreads) hist[i] = 0.f;
   if (threadIdx.x == 0) {
     br.abort = 0;
     mbar_init(&br.tile_full, 1);
-    for (int s = 0; s < kSbSlots; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(&br.full[s], 2);
       mbar_init(&br.empty[s], 1);
     }
@@ -426,8 +474,8 @@ __global__ void __launch_bounds__(kSbThreads, 1)
       }
       int last = -1;
       for (int j = 0; j < nblk; ++j) {
-        const int s = j % kSbSlots;
-        if (j >= kSbSlots && !mbar_wait(&br.empty[s], (j / kSbSlots - 1) & 1, abort)) {
+        const int s = j % kSlots;
+        if (j >= kSlots && !mbar_wait(&br.empty[s], (j / kSlots - 1) & 1, abort)) {
           fail_s(a.status, &br.abort, kDevErrTimeoutLoad);
           break;
         }
@@ -448,8 +496,8 @@ __global__ void __launch_bounds__(kSbThreads, 1)
         if (!kQ && warp == 0) {
           for (int m = 0; m < NM; ++m) {
             const size_t off = (size_t(m) * g.BH + bh) * g.S + size_t(blk) * 64;
-            bulk_load(&sm.lse2[s][m][0], a.lse2 + off, 256u, &br.full[s]);
-            bulk_load(&sm.dsum[s][m][0], a.dsum + off, 256u, &br.full[s]);
+            bulk_load(&sm.nlse[s][m][0], a.nlse + off, 256u, &br.full[s]);
+            bulk_load(&sm.ndsum[s][m][0], a.ndsum + off, 256u, &br.full[s]);
           }
         }
         last = j;
@@ -459,8 +507,8 @@ __global__ void __launch_bounds__(kSbThreads, 1)
         // the abort flag): at most the last use of each slot is open
         int never = 0;
         if (warp == 0) mbar_wait(&br.tile_full, 0, &never);
-        for (int jj = last; jj >= 0 && jj > last - kSbSlots; --jj)
-          mbar_wait(&br.full[jj % kSbSlots], (jj / kSbSlots) & 1, &never);
+        for (int jj = last; jj >= 0 && jj > last - kSlots; --jj)
+          mbar_wait(&br.full[jj % kSlots], (jj / kSlots) & 1, &never);
       }
     }
   } else if (warp == 1) {
@@ -481,7 +529,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
       const uint64_t b1_mn = sw128_desc(smem_u32(&sm.sa[0][0][0]), kBlk, 1024);
       const uint64_t b2_mn = sw128_desc(smem_u32(&sm.sb[0][0][0]), kBlk, 1024);
       auto where = [&](int i) -> uint64_t {
-        return uint64_t((i / kHalves) % kSbSlots) * kSlot + uint64_t(i % kHalves) * kHalf;
+        return uint64_t((i / kHalves) % kSlots) * kSlot + uint64_t(i % kHalves) * kHalf;
       };
       const bool one = elect_one();
       auto issue = [&](int i) {
@@ -506,7 +554,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
           const int j = (i + 1) / kHalves;
           if ((i + 1) % kHalves == 0)
             ok = __all_sync(0xFFFFFFFFu,
-                            mbar_wait(&br.full[j % kSbSlots], (j / kSbSlots) & 1, abort));
+                            mbar_wait(&br.full[j % kSlots], (j / kSlots) & 1, abort));
           if (!ok) break;
           tc_fence_after_sync();
           issue(i + 1);
@@ -527,7 +575,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
           mma_from_tmem<W / 16>(tmem + kColY + 64u * m, st + kDP + 8u * m,
                                 b1_mn + where(i) + m * kMap, id_y, acc);
         }
-        if ((i + 1) % kHalves == 0) mma_commit(&br.empty[(i / kHalves) % kSbSlots]);
+        if ((i + 1) % kHalves == 0) mma_commit(&br.empty[(i / kHalves) % kSlots]);
         }
         __syncwarp();
       }
@@ -550,48 +598,66 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     const bool valid = r < 64 || bb >= 0;          // uniform across the warp
     const int blk = r < 64 || bb < 0 ? ba : bb;
     const int my_keep = !valid ? 0 : r < 64 ? kEntryKeepA : kEntryKeepB;
-    const float sl2 = a.scale_log2;
+    const uint64_t sl2x2 = f2_pack(a.scale_log2, a.scale_log2);
     const float lam = kDiff ? __bfloat162float(a.lam[bh % a.H]) : 0.f;
+    const uint64_t nlam2 = f2_pack(-lam, -lam);
     const size_t my_pos = size_t(bh) * g.S + size_t(blk) * 64 + (r & 63);
-    float lse2[NM], dsum[NM], dfull[NM];  // query pass: this row's
+    float nlse[NM], ndsum[NM];  // query pass: this row's
+    uint64_t dfull2[NM];
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
-      lse2[m] = kQ ? a.lse2[size_t(m) * g.BH * g.S + my_pos] : 0.f;
-      dsum[m] = kQ ? a.dsum[size_t(m) * g.BH * g.S + my_pos] : 0.f;
-      dfull[m] = 0.f;
+      nlse[m] = kQ ? a.nlse[size_t(m) * g.BH * g.S + my_pos] : 0.f;
+      ndsum[m] = kQ ? a.ndsum[size_t(m) * g.BH * g.S + my_pos] : 0.f;
+      dfull2[m] = 0ull;
     }
     constexpr int kSign = kQ ? 1 : -1;
+    constexpr int kG = Cols<L>::kG, kF = Cols<L>::kF;
     RelBiasRow rb;
-    if constexpr (!kDiff) rb = relbias_row(g, blk, r & 63, kSign);
+    float* my_hist = hist + (warp - 4) * hist_floats(g);
+    int to_h = 0, to_w = 0, to_t = 0;  // from an offset's index in the tables to the histogram's
+    if constexpr (!kDiff) {
+      rb = relbias_row(g, blk, r & 63, kSign);
+      int t, hp, wp;
+      block_coords(g, blk, t, hp, wp);
+      to_t = t * g.pt;
+      to_h = g.T - g.pt + hp * g.ph;
+      to_w = (g.T - g.pt) + (g.Hh - g.ph) + wp * g.pw;
+    }
     const uint32_t st = lane_base + kStage0 + kStage * uint32_t(grp);
     bool ok = true;
     for (int i = grp; i < n; i += 2) {
-      const int j = i / kHalves, s = j % kSbSlots;
+      const int j = i / kHalves, s = j % kSlots;
       const int ent = at(j);
       const bool keep = (ent & my_keep) != 0;  // uniform across the warp
-      ok = __all_sync(0xFFFFFFFFu,
-                      mbar_wait(&br.s_full[grp], (i >> 1) & 1, abort) &&
-                          (kQ || mbar_wait(&br.full[s], (j / kSbSlots) & 1, abort)));
-      if (!ok) break;
-      tc_fence_after_sync();
-      float f[Cols<L>::kF], c[Cols<L>::kG], gf[Cols<L>::kF], gc[Cols<L>::kG];
+      // the bias of this thread's columns, while the scores are computed: f per
+      // run, c per column in pairs (query pass: the row's -lse with it)
+      float f[kF], c[kG];
       int it = 0, ih = 0, iw = 0;
       if constexpr (!kDiff) {
         if (keep) {
           relbias_block(g, rb, ent & kEntryBlockMask, kSign, it, ih, iw);
           load_bias32<L>(bias, g, it, ih, iw, wg, kSign, f, c);
-          if constexpr (kTable) {
+          if (kQ) {
 #pragma unroll
-            for (int x = 0; x < Cols<L>::kF; ++x) gf[x] = 0.f;
-#pragma unroll
-            for (int y = 0; y < Cols<L>::kG; ++y) gc[y] = 0.f;
+            for (int y = 0; y < kG; ++y) c[y] += nlse[0];
           }
         }
       }
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&br.s_full[grp], (i >> 1) & 1, abort) &&
+                                       (kQ || mbar_wait(&br.full[s], (j / kSlots) & 1, abort)));
+      if (!ok) break;
+      tc_fence_after_sync();
+      uint64_t gf2[kF], gc2[(kG + 1) / 2];
+      if constexpr (kTable) {
+#pragma unroll
+        for (int x = 0; x < kF; ++x) gf2[x] = 0ull;
+#pragma unroll
+        for (int y = 0; y < (kG + 1) / 2; ++y) gc2[y] = 0ull;
+      }
 #pragma unroll
       for (int ch = 0; ch < W / 32; ++ch) {
-        const int col = (W / 2) * wg + 16 * ch;                       // in the stage
-        const int qcol = (kDiff ? 32 * (i % kHalves) : 0) + col;      // in the streamed block
+        const int col = (W / 2) * wg + 16 * ch;                   // in the stage
+        const int qcol = (kDiff ? 32 * (i % kHalves) : 0) + col;  // in the streamed block
         uint32_t pk[NM][8], ds[NM][8];
         if (keep) {
           uint32_t x[NM][16], dp[16];
@@ -601,42 +667,42 @@ __global__ void __launch_bounds__(kSbThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
-            float pp[NM][2], dd[NM][2];
+            const uint64_t e2 = f2_pack(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1]));
+            uint64_t p2[NM];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float e = __uint_as_float(dp[k + u]);
-#pragma unroll
-              for (int m = 0; m < NM; ++m) {
-                const float ls = kQ ? lse2[m] : sm.lse2[s][m][qcol + k + u];
-                const float dm = kQ ? dsum[m] : sm.dsum[s][m][qcol + k + u];
-                float z;
-                if constexpr (kDiff) {
-                  z = fmaf(__uint_as_float(x[m][k + u]), sl2, -ls);
-                } else {
-                  const int q = 16 * ch + k + u;
-                  z = fmaf(__uint_as_float(x[m][k + u]), sl2,
-                           f[q / Cols<L>::kG] + (c[q % Cols<L>::kG] - ls));
-                }
-                const float p = ex2_approx(z);
-                if (kQ) dfull[m] = fmaf(p, e, dfull[m]);
-                const float w = m == 0 ? p : lam * p;
-                pp[m][u] = kQ ? p : w;
-                dd[m][u] = m == 0 ? w * (e - dm) : w * (dm - e);
-                if constexpr (kTable) {
-                  const int q = 16 * ch + k + u;
-                  gf[q / Cols<L>::kG] += dd[0][u];
-                  gc[q % Cols<L>::kG] += dd[0][u];
-                }
+            for (int m = 0; m < NM; ++m) {
+              uint64_t nl2, nd2;
+              if (kQ) {
+                nl2 = f2_pack(nlse[m], nlse[m]);
+                nd2 = f2_pack(ndsum[m], ndsum[m]);
+              } else {
+                nl2 = *reinterpret_cast<const uint64_t*>(&sm.nlse[s][m][qcol + k]);
+                nd2 = *reinterpret_cast<const uint64_t*>(&sm.ndsum[s][m][qcol + k]);
+              }
+              if constexpr (!kDiff) {
+                const int q = 16 * ch + k;
+                const uint64_t f2 = f2_pack(f[q / kG], f[(q + 1) / kG]);
+                const uint64_t c2 = f2_pack(c[q % kG], c[(q + 1) % kG]);
+                nl2 = kQ ? f2_add(f2, c2) : f2_add(f2_add(f2, c2), nl2);
+              }
+              p2[m] = f2_ex2(f2_fma(
+                  f2_pack(__uint_as_float(x[m][k]), __uint_as_float(x[m][k + 1])), sl2x2, nl2));
+              if (kQ) dfull2[m] = f2_fma(p2[m], e2, dfull2[m]);
+              // (map 2: -lambda is applied to the finished dQ_2 and dK_2)
+              const uint64_t d2 = f2_mul(p2[m], f2_add(e2, nd2));
+              ds[m][k / 2] = f2_bf16(d2);
+              if constexpr (kTable) {
+                const int q = 16 * ch + k;
+                gf2[kG > 1 ? q / kG : q / 2] = f2_add(gf2[kG > 1 ? q / kG : q / 2], d2);
+                gc2[(q % kG) / 2] = f2_add(gc2[(q % kG) / 2], d2);
               }
             }
             if constexpr (kDiff && !kQ) {
-              pk[0][k / 2] = pack_bf16x2(pp[0][0] - pp[NM - 1][0], pp[0][1] - pp[NM - 1][1]);
+              pk[0][k / 2] = f2_bf16(f2_fma(nlam2, p2[NM - 1], p2[0]));
             } else {
 #pragma unroll
-              for (int m = 0; m < NM; ++m) pk[m][k / 2] = pack_bf16x2(pp[m][0], pp[m][1]);
+              for (int m = 0; m < NM; ++m) pk[m][k / 2] = f2_bf16(p2[m]);
             }
-#pragma unroll
-            for (int m = 0; m < NM; ++m) ds[m][k / 2] = pack_bf16x2(dd[m][0], dd[m][1]);
           }
         } else {
 #pragma unroll
@@ -653,14 +719,29 @@ __global__ void __launch_bounds__(kSbThreads, 1)
       tmem_wait_st();
       warp_arrive(&br.out_full[grp], lane);
       if constexpr (kTable) {
-        if (keep) add_table_grad<L>(hist, g, it, ih, iw, wg, lane, gf, gc);
+        if (keep) {
+#pragma unroll
+          for (int x = 0; x < kF; ++x) {
+            float lo, hi;
+            f2_unpack(gf2[kG > 1 ? x : x / 2], lo, hi);
+            f[x] = kG > 1 ? lo + hi : (x & 1 ? hi : lo);
+          }
+#pragma unroll
+          for (int y = 0; y < kG; ++y) {
+            float lo, hi;
+            f2_unpack(gc2[y / 2], lo, hi);
+            c[y] = kG == 1 ? lo + hi : (y & 1 ? hi : lo);
+          }
+          add_table_grad<L>(my_hist, g, it - to_t, ih - to_h, iw - to_w, wg, lane, f, c);
+        }
       }
     }
+    float dfull[NM];
     if (kQ && ok) {
       // D of every row: four warps' partial sums, in a fixed order
-      float* sums = &sm.lse2[0][0][0];  // [map][part][row]
+      float* sums = &sm.nlse[0][0][0];  // [map][part][row]
 #pragma unroll
-      for (int m = 0; m < NM; ++m) sums[(m * 4 + part) * 128 + r] = dfull[m];
+      for (int m = 0; m < NM; ++m) sums[(m * 4 + part) * 128 + r] = f2_sum(dfull2[m]);
       warp_arrive(&br.dsum_full, lane);
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&br.dsum_full, 0, abort));
       if (ok) {
@@ -676,7 +757,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     } else if (valid) {  // uniform across the warp
       if (kQ && part == 0) {
 #pragma unroll
-        for (int m = 0; m < NM; ++m) a.dsum[size_t(m) * g.BH * g.S + my_pos] = dfull[m];
+        for (int m = 0; m < NM; ++m) a.ndsum[size_t(m) * g.BH * g.S + my_pos] = -dfull[m];
       }
       if (32 * part < D) {
         if (n > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&br.acc_full, 0, abort))) {
@@ -686,15 +767,15 @@ __global__ void __launch_bounds__(kSbThreads, 1)
           const int c = 32 * part;
           const size_t dst = (size_t(bh) * g.S + block_row_token(g, blk, r & 63)) * D + c;
           const uint32_t y = lane_base + kColY + acc_col<D, kDiff>(c);
+          const bool second = kDiff && c >= D / 2;
+          const float mul = second ? -lam * a.scale : a.scale;  // dS_2 = -lambda P_2 (dP - D_2)
           if constexpr (kQ) {
-            const int m = kDiff && c >= D / 2 ? NM - 1 : 0;
-            float fix = dfull[m] - dsum[m];
-            if (kDiff && m > 0) fix *= -lam;  // dS_2 = -lambda P_2 (dP - D_2)
-            store_acc32(y, lane_base + kColX + acc_col<D, kDiff>(c), n > 0, a.scale, fix, a.dq, dst,
+            const float fix = second ? dfull[NM - 1] + ndsum[NM - 1] : dfull[0] + ndsum[0];
+            store_acc32(y, lane_base + kColX + acc_col<D, kDiff>(c), n > 0, mul, fix, a.dq, dst,
                         a.out_fp32);
           } else {
             store_acc32(lane_base + kColX + c, 0u, n > 0, 1.f, 0.f, a.dv, dst, a.out_fp32);
-            store_acc32(y, 0u, n > 0, a.scale, 0.f, a.dk, dst, a.out_fp32);
+            store_acc32(y, 0u, n > 0, mul, 0.f, a.dk, dst, a.out_fp32);
           }
         }
       }
@@ -705,8 +786,28 @@ __global__ void __launch_bounds__(kSbThreads, 1)
   tc_fence_after_sync();
   if (warp == 1) tmem_dealloc(tmem, 512);
   if constexpr (kTable) {
+    // the 16 warps' histograms (8 per block of the tile) joined in a fixed order
     float* dst = a.part + unit * noff;
-    for (int i = threadIdx.x; i < noff; i += kSbThreads) dst[i] = hist[i];
+    int o[2][3];  // table index - histogram index, per block and axis
+    for (int e = 0; e < 2; ++e) {
+      int t, hp, wp;
+      block_coords(g, e == 0 || bb < 0 ? ba : bb, t, hp, wp);
+      o[e][0] = t * g.pt;
+      o[e][1] = g.T - g.pt + hp * g.ph;
+      o[e][2] = (g.T - g.pt) + (g.Hh - g.ph) + wp * g.pw;
+    }
+    const int nt = g.T + g.pt - 1, nh = g.Hh + g.ph - 1, per = hist_floats(g);
+    for (int i = threadIdx.x; i < noff; i += kSbThreads) {
+      const int axis = i < 2 * g.T - 1 ? 0 : i < 2 * g.T - 1 + 2 * g.Hh - 1 ? 1 : 2;
+      const int lo = axis == 0 ? 0 : axis == 1 ? nt : nt + nh;
+      const int hi = axis == 0 ? nt : axis == 1 ? nt + nh : per;
+      float sum = 0.f;
+      for (int w = 0; w < kSbRowWarps; ++w) {
+        const int k = i - o[(w & 3) >> 1][axis];  // quads 2 and 3 are the second block
+        if (k >= lo && k < hi) sum += hist[w * per + k];
+      }
+      dst[i] = sum;
+    }
   }
 }
 
@@ -750,7 +851,7 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// dlambda[h] = -sum of D_2 (dsum's second map, [BH][S]) over the batch and the
+// dlambda[h] = sum of -D_2 (ndsum's second map, [BH][S]) over the batch and the
 // rows, in a fixed order. One CTA per head.
 __global__ void __launch_bounds__(1024)
     dlambda_kernel(const float* __restrict__ d2, int S, int B, int H, void* __restrict__ dlam,
@@ -775,8 +876,8 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
     if (lane == 0) {
-      if (fp32) static_cast<float*>(dlam)[h] = -s;
-      else static_cast<__nv_bfloat16*>(dlam)[h] = __float2bfloat16_rn(-s);
+      if (fp32) static_cast<float*>(dlam)[h] = s;
+      else static_cast<__nv_bfloat16*>(dlam)[h] = __float2bfloat16_rn(s);
     }
   }
 }
@@ -785,9 +886,12 @@ template <int D, AttnMode M, int L, bool kQ>
 static cudaError_t launch_pass(const ScoreBwdArgs& a, const Geometry& g, cudaStream_t stream) {
   // the offset tables, and in the key pass the histogram behind them; at least
   // 120 KB, since each CTA allocates all 512 TMEM columns
+  constexpr bool kTable = M != AttnMode::kDiff && !kQ;
   const size_t tables =
-      M == AttnMode::kDiff ? 0 : (kQ ? 1 : 2) * relbias_offsets(g) * sizeof(float);
-  const size_t need = sizeof(SbSmem<D>) + 1024 + tables;
+      M == AttnMode::kDiff
+          ? 0
+          : sizeof(float) * (relbias_offsets(g) + (kTable ? kSbRowWarps * hist_floats(g) : 0));
+  const size_t need = sizeof(SbSmem<D, kTable ? 3 : kSbSlots>) + 1024 + tables;
   const int smem = int(need > 120 * 1024 ? need : 120 * 1024);
   cudaError_t e = cudaFuncSetAttribute(score_bwd_kernel<D, M, L, kQ>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -822,7 +926,7 @@ cudaError_t launch_score_bwd(const ScoreBwdArgs& a, const Geometry& g, cudaStrea
   const bool diff = a.lam != nullptr;
 #define SA_PREP(D, DIFF)                                                                       \
   score_prep_kernel<D, DIFF><<<grid, 256, 0, stream>>>(a.out, a.out2, a.dout, a.lse, a.lam, a.H, \
-                                                       a.lse2, a.dsum, a.out_fp32, g)
+                                                       a.nlse, a.ndsum, a.out_fp32, g)
   if (g.d == 128) {
     if (diff) SA_PREP(128, true); else SA_PREP(128, false);
   } else {
@@ -835,7 +939,7 @@ cudaError_t launch_score_bwd(const ScoreBwdArgs& a, const Geometry& g, cudaStrea
     e = g.d == 128 ? launch_score_bwd_d<128>(a, g, stream) : launch_score_bwd_d<64>(a, g, stream);
   if (e != cudaSuccess) return e;
   if (diff)
-    dlambda_kernel<<<unsigned(a.H), 1024, 0, stream>>>(a.dsum + size_t(g.BH) * g.S, g.S,
+    dlambda_kernel<<<unsigned(a.H), 1024, 0, stream>>>(a.ndsum + size_t(g.BH) * g.S, g.S,
                                                        g.BH / a.H, a.H, a.dparam, a.out_fp32);
   else
     dtable_kernel<<<unsigned(a.H), 1024, 0, stream>>>(a.part, a.bias, g.BH / a.H, a.dparam,

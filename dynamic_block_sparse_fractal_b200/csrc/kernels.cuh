@@ -81,9 +81,9 @@ enum class AttnMode { kPlain, kBias, kBias8, kDiff };
 // through bucket[], the table index of every offset along t, then h, then w
 // ((2T-1) + (2Hh-1) + (2Ww-1) entries, offset key - query, lowest first).
 // Offsets along the three axes, and the most that the kernels' shared memory
-// holds (T + Hh + Ww <= 1152).
+// holds (T + Hh + Ww <= 640).
 SA_HD int relbias_offsets(const Geometry& g) { return 2 * (g.T + g.Hh + g.Ww) - 3; }
-constexpr int kRelBiasMaxAxes = 1152;
+constexpr int kRelBiasMaxAxes = 640;
 struct BiasArgs {
   const __nv_bfloat16* table;  // null: no bias
   const int32_t* bucket;
@@ -182,8 +182,8 @@ struct ScoreBwdArgs {
   const void* out2;
   const __nv_bfloat16* dout;
   const float* lse;
-  float* lse2;  // [maps][BH][S] fractal order, log2 units
-  float* dsum;  // [maps][BH][S] fractal order: rowsum(dO * P_m V)
+  float* nlse;   // [maps][BH][S] fractal order: -lse, log2 units
+  float* ndsum;  // [maps][BH][S] fractal order: -rowsum(dO * P_m V)
   float* part;  // bias: [BH][ntile][offsets]
   int32_t* kcnt;
   int32_t* kidx;
@@ -207,13 +207,13 @@ struct ScoreBwdArgs {
 cudaError_t launch_score_bwd(const ScoreBwdArgs& a, const Geometry& g, cudaStream_t stream);
 
 struct ScoreBwdLayout {
-  size_t lse2, dsum, kcnt, kidx, part, total;
+  size_t nlse, ndsum, kcnt, kidx, part, total;
 };
 inline ScoreBwdLayout make_score_bwd_layout(const Geometry& g, int maps, size_t parts_per_head) {
   ScoreBwdLayout b;
   size_t o = 0;
-  b.lse2 = o; o = align256(o + sizeof(float) * maps * size_t(g.BH) * g.S);
-  b.dsum = o; o = align256(o + sizeof(float) * maps * size_t(g.BH) * g.S);
+  b.nlse = o; o = align256(o + sizeof(float) * maps * size_t(g.BH) * g.S);
+  b.ndsum = o; o = align256(o + sizeof(float) * maps * size_t(g.BH) * g.S);
   b.kcnt = o; o = align256(o + sizeof(int32_t) * size_t(g.BH) * g.ntile);
   b.kidx = o; o = align256(o + sizeof(int32_t) * size_t(g.BH) * g.ntile * g.nb);
   b.part = o; o = align256(o + sizeof(float) * size_t(g.BH) * parts_per_head);

@@ -459,14 +459,14 @@ typedef struct sa_rel_bias {
 
 /* sparse_attn_fwd with the bias. lse (may be NULL): as for sparse_attn_fwd_lse,
  * of the biased scores. The workspace holds any plan made for the same desc.
- * SA_ERR_UNSUPPORTED when T + Hh + Ww > 1152. A row whose kept offsets are all
+ * SA_ERR_UNSUPPORTED when T + Hh + Ww > 640. A row whose kept offsets are all
  * masked is treated as one that keeps nothing. */
 sa_status sparse_attn_fwd_bias(const sa_desc* desc, const sa_rel_bias* bias, const void* q,
                                const void* k, const void* v, const void* workspace,
                                size_t ws_bytes, void* out, float* lse, void* stream);
 
 /* Bytes of device scratch sparse_attn_bwd_bias needs: two fp32 [B*H][S] row
- * statistics, the transposed block lists, and one partial sum per query tile
+ * statistics, the transposed block lists, and one partial sum per key tile
  * and offset. */
 sa_status sparse_attn_bwd_bias_scratch_size(const sa_desc* desc, size_t* bytes);
 
@@ -474,9 +474,9 @@ sa_status sparse_attn_bwd_bias_scratch_size(const sa_desc* desc, size_t* bytes);
  * biased scores, and dtable [H][n_buckets] (bf16, fp32 if desc->out_fp32,
  * 4-byte aligned, overwritten): the sum of dS = P (dP - D) over the batch and
  * over every kept pair whose offset along an axis falls into the bucket, axis
- * by axis. dq, dk and dv are the same bits at every run of the same inputs;
- * dtable's sums of one query tile are fp32 additions in no fixed order. out,
- * lse: what sparse_attn_fwd_bias wrote. Scratch as for sparse_attn_bwd, of
+ * by axis. dq, dk and dv are the same bits at every run of the same inputs,
+ * and so is dtable unless a block spans several frames (pt > 1: some fp32
+ * additions in no fixed order). out, lse: what sparse_attn_fwd_bias wrote. Scratch as for sparse_attn_bwd, of
  * sparse_attn_bwd_bias_scratch_size() bytes. */
 sa_status sparse_attn_bwd_bias(const sa_desc* desc, const sa_rel_bias* bias, const void* q,
                                const void* k, const void* v, const void* out, const void* dout,
