@@ -732,6 +732,38 @@ class NablaAttention:
         """(dq, dk, dv) of sum(out * dout) over the current plan's mask."""
         return bwd(self.desc, q, k, v, out, dout, lse, self.workspace, stream=stream)
 
+    def plan_mask(self, mask, stream=None):
+        """Plan from the caller's own block mask (see ``plan_mask``)."""
+        plan_mask(self.desc, mask, self.workspace, stream)
+
+    def forward_bias(self, q, k, v, table, bucket, out=None, lse=None, stream=None):
+        """Forward with a learned relative position bias over the current plan, with
+        each row's log-sum-exp: (out, lse)."""
+        if lse is None:
+            lse = _new(q.shape[:3], torch.float32, q.device, stream)
+        return fwd_bias(self.desc, q, k, v, table, bucket, self.workspace, out, lse, stream), lse
+
+    def backward_bias(self, q, k, v, table, bucket, out, dout, lse, stream=None):
+        """(dq, dk, dv, dtable) of sum(out * dout) over the current plan's mask."""
+        return bwd_bias(self.desc, q, k, v, table, bucket, out, dout, lse, self.workspace,
+                        stream=stream)
+
+    def forward_diff(self, q, k, v, lam, out=None, out2=None, lse=None, stream=None):
+        """Differential attention over the current plan, with what ``backward_diff``
+        reads: (out, out2, lse)."""
+        if out2 is None:
+            out2 = _new(q.shape, torch.float32 if self.desc.out_fp32 else torch.bfloat16, q.device,
+                        stream)
+        if lse is None:
+            lse = _new((2,) + tuple(q.shape[:3]), torch.float32, q.device, stream)
+        out = fwd_diff(self.desc, q, k, v, lam, self.workspace, out, out2, lse, stream)
+        return out, out2, lse
+
+    def backward_diff(self, q, k, v, lam, out, out2, dout, lse, stream=None):
+        """(dq, dk, dv, dlam) of sum(out * dout) over the current plan's mask."""
+        return bwd_diff(self.desc, q, k, v, lam, out, out2, dout, lse, self.workspace,
+                        stream=stream)
+
     def heatmap(self, q, k, stream=None):
         """Exact block max-pooled full-attention map [B*H, nb, nb]."""
         return block_heatmap(self.desc, q, k, self.workspace, stream=stream)

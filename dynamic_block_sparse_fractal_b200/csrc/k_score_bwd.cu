@@ -98,8 +98,9 @@ __device__ __forceinline__ void mma_from_tmem(uint32_t d_tmem, uint32_t a_tmem, 
     mma_ts(d_tmem, a_tmem + uint32_t(kk) * 16u, b + uint64_t(kk) * 128u, id, kk > 0 ? 1u : acc);
 }
 
-// mul * (32 accumulator columns of this lane's row - fix * 32 columns at `sub`)
-// (zeros without a step) -> 32 elements of an output, bf16 or fp32.
+// mul * (32 accumulator columns of this lane's row, kFix: less fix * 32 columns at
+// `sub`; zeros without a step) -> 32 elements of an output, bf16 or fp32.
+template <bool kFix>
 __device__ __forceinline__ void store_acc32(uint32_t col, uint32_t sub, bool any, float mul,
                                             float fix, void* out, size_t at, int fp32) {
   float x[32];
@@ -109,7 +110,7 @@ __device__ __forceinline__ void store_acc32(uint32_t col, uint32_t sub, bool any
     tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
-    if (sub != 0u) {
+    if constexpr (kFix) {
       tmem_ld32(sub, o);
       tmem_wait_ld();
 #pragma unroll
@@ -771,11 +772,11 @@ __global__ void __launch_bounds__(kSbThreads, 1)
           const float mul = second ? -lam * a.scale : a.scale;  // dS_2 = -lambda P_2 (dP - D_2)
           if constexpr (kQ) {
             const float fix = second ? dfull[NM - 1] + ndsum[NM - 1] : dfull[0] + ndsum[0];
-            store_acc32(y, lane_base + kColX + acc_col<D, kDiff>(c), n > 0, mul, fix, a.dq, dst,
+            store_acc32<true>(y, lane_base + kColX + acc_col<D, kDiff>(c), n > 0, mul, fix, a.dq, dst,
                         a.out_fp32);
           } else {
-            store_acc32(lane_base + kColX + c, 0u, n > 0, 1.f, 0.f, a.dv, dst, a.out_fp32);
-            store_acc32(y, 0u, n > 0, mul, 0.f, a.dk, dst, a.out_fp32);
+            store_acc32<false>(lane_base + kColX + c, 0u, n > 0, 1.f, 0.f, a.dv, dst, a.out_fp32);
+            store_acc32<false>(y, 0u, n > 0, mul, 0.f, a.dk, dst, a.out_fp32);
           }
         }
       }

@@ -1,5 +1,6 @@
 """CPU fp64 oracle for NABLA block-sparse video attention (nabla.py) and for
-the Token Radius Attention block mask (tra.py).
+the Token Radius Attention block mask (tra.py), and of the biased and the
+differential attention (score.py).
 
 TEST INFRASTRUCTURE ONLY: the reference the CUDA path is checked against.
 Only the tests, the smoke check and the benchmark's CPU-baseline leg may
@@ -14,3 +15,4 @@ from .nabla import (  # noqa: F401
 from .tra import (  # noqa: F401
     token_entropy, entropy_budget, budget_radius2, radius_support, radius_block_mask, tra_mask,
 )
+from . import score  # noqa: F401
