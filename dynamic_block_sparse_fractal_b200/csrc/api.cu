@@ -502,6 +502,7 @@ static sa_status score_bwd_impl(const sa_desc* desc, const BiasArgs& bias, const
   a.part = at<float>(scratch, b.part);
   a.kcnt = at<int32_t>(scratch, b.kcnt);
   a.kidx = at<int32_t>(scratch, b.kidx);
+  a.korder = at<int32_t>(scratch, b.korder);
   a.bits = at<uint32_t>(workspace, w.bits);
   a.tcnt = at<int32_t>(workspace, w.tcnt);
   a.tidx = at<int32_t>(workspace, w.tidx);

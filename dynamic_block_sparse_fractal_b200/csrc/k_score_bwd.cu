@@ -214,6 +214,52 @@ __device__ __forceinline__ int lane_sums(float (&v)[N], int lane, int& first, bo
 // that no atomics are needed (histograms shared by the CTA's warps with atomic
 // additions took 4,500 cycles a step, three times the step's products). Blocks
 // of several frames can still meet at an address and add atomically.
+// The same for blocks of one frame with rows of 8 (the 8 x 8 patch). A warp holds
+// 4 rows x 8 columns of keys against 4 rows x 8 columns of queries: 1 + 7 + 15
+// offsets. The sums over one axis are brought together along their diagonals by
+// shuffles, so that one addition to the histogram, each lane at an address of its
+// own, ends the step. The frame offset's sum stays in a register (tsum, at index
+// tcur) until another frame comes, which the ascending list makes rare.
+__device__ __forceinline__ void add_table_grad_patch(float* hist, int h, int w, int wg, int lane,
+                                                     const float (&f)[4], const float (&c)[8]) {
+  constexpr unsigned kAll = 0xFFFFFFFFu;
+  // rows: lane 8 a + 2 x holds the sum over the columns of key row a, query row x
+  const bool u2 = lane & 4, u1 = lane & 2, u4 = lane & 16;
+  const float a0 = (u2 ? f[2] : f[0]) + __shfl_xor_sync(kAll, u2 ? f[0] : f[2], 4);
+  const float a1 = (u2 ? f[3] : f[1]) + __shfl_xor_sync(kAll, u2 ? f[1] : f[3], 4);
+  float v = (u1 ? a1 : a0) + __shfl_xor_sync(kAll, u1 ? a0 : a1, 2);
+  v += __shfl_xor_sync(kAll, v, 1);
+  // columns: bit 4 halves the 8 sums (query columns 4 up ..), bit 3 is summed over;
+  // then a half-warp's sums run along their diagonal, one lane on at each addition:
+  // lane p of half up holds the offset p - 3 - 4 up
+  float r = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float x = (u4 ? c[k + 4] : c[k]) + __shfl_xor_sync(kAll, u4 ? c[k] : c[k + 4], 16);
+    x += __shfl_xor_sync(kAll, x, 8);
+    if (k > 0) {
+      r = __shfl_up_sync(kAll, r, 1, 16);
+      if ((lane & 15) == 0) r = 0.f;
+    }
+    if (!(lane & 8)) r += x;
+  }
+  // lane p < 7: row offset p - 3; lanes 8 .. 22: column offset lane - 15
+  float s = 0.f;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int a = lane - 3 + x;
+    const float y = __shfl_sync(kAll, v, (8 * a + 2 * x) & 31);
+    if (a >= 0 && a < 4) s += y;
+  }
+  const int o = lane - 8;
+  const float lo = __shfl_sync(kAll, r, (o - 4) & 15), hi = __shfl_sync(kAll, r, 16 + (o & 15));
+  if (lane >= 8) s = (o >= 4 ? lo : 0.f) + (o <= 10 ? hi : 0.f);
+  // h, w: this lane's indexes for query row and column 0 (key row lane >> 3, column lane & 7)
+  const int at = lane < 8 ? h - 4 * wg + lane - 3 : w - (lane & 7) + o - 7;
+  if (lane != 7 && o <= 14) hist[at] += s;
+  __syncwarp();
+}
+
 template <int L>
 __device__ __forceinline__ void add_table_grad(float* hist, const Geometry& g, int t, int h, int w,
                                                int wg, int lane, float (&f)[Cols<L>::kF],
@@ -232,7 +278,8 @@ __device__ __forceinline__ void add_table_grad(float* hist, const Geometry& g, i
   int n = lane_sums<NF, 0, L>(f, lane, first, writer);  // lanes of one row run
   if (g.pt == 1) {
     // lanes of equal column bits are different rows of the block
-    for (int q = 0; q < 1 << L; ++q) {
+    constexpr int kStep = NF >= 1 << L ? 1 : (1 << L) / NF;  // (the others are no writers)
+    for (int q = 0; q < 1 << L; q += kStep) {
       if (writer && (lane & ((1 << L) - 1)) == q) {
 #pragma unroll
         for (int k = 0; k < NF; ++k)
@@ -412,9 +459,12 @@ __global__ void __launch_bounds__(kSbThreads, 1)
   const int noff = relbias_offsets(g);
   float* hist = bias + noff;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = blockIdx.y;
-  // (query tiles heaviest first)
-  const int tile = kQ ? a.order[size_t(bh) * g.ntile + blockIdx.x] : int(blockIdx.x);
+  // CTAs start heaviest tile first over a group of heads (see launch_pass)
+  const int first_head = int(blockIdx.x) / (a.group * g.ntile) * a.group;
+  const int heads = min(a.group, g.BH - first_head);
+  const int in_group = int(blockIdx.x) - first_head * g.ntile;
+  const int bh = first_head + in_group % heads;
+  const int tile = (kQ ? a.order : a.korder)[size_t(bh) * g.ntile + in_group / heads];
   int ba, bb;  // the tile's blocks (bb = -1: a lone block)
   tile_blocks(g, tile, ba, bb);
   const size_t unit = size_t(bh) * g.ntile + tile;
@@ -533,9 +583,8 @@ __global__ void __launch_bounds__(kSbThreads, 1)
         return uint64_t((i / kHalves) % kSlots) * kSlot + uint64_t(i % kHalves) * kHalf;
       };
       const bool one = elect_one();
-      auto issue = [&](int i) {
+      auto issue = [&](int i) {  // S and dP of step i
         const uint32_t st = tmem + kStage0 + kStage * uint32_t(i & 1);
-        if (!one) return;
 #pragma unroll
         for (int m = 0; m < NM; ++m)
           mma_scores<D / 16 / NM>(st + W * m, a1, kTile, b1 + where(i), kBlk, id_s,
@@ -543,40 +592,49 @@ __global__ void __launch_bounds__(kSbThreads, 1)
         mma_scores<D / 16>(st + kDP, a2, kTile, b2 + where(i), kBlk, id_s, 0);
         mma_commit(&br.s_full[i & 1]);
       };
-      bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&br.tile_full, 0, abort) &&
-                                            mbar_wait(&br.full[0], 0, abort));
+      bool ok = mbar_wait(&br.tile_full, 0, abort) && mbar_wait(&br.full[0], 0, abort);
+      if (kHalves == 1 && n > 1) ok = ok && mbar_wait(&br.full[1 % kSlots], 0, abort);
+      ok = __all_sync(0xFFFFFFFFu, ok);
       if (ok) {
         tc_fence_after_sync();
-        issue(0);
-      }
-      for (int i = 0; ok && i < n; ++i) {
-        if (i + 1 < n) {
-          // stage (i + 1) & 1 was last read by step i - 1's products, issued before
-          const int j = (i + 1) / kHalves;
-          if ((i + 1) % kHalves == 0)
-            ok = __all_sync(0xFFFFFFFFu,
-                            mbar_wait(&br.full[j % kSlots], (j / kSlots) & 1, abort));
-          if (!ok) break;
-          tc_fence_after_sync();
-          issue(i + 1);
-        }
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&br.out_full[i & 1], (i >> 1) & 1, abort));
-        if (!ok) break;
-        tc_fence_after_sync();
-        const uint32_t st = tmem + kStage0 + kStage * uint32_t(i & 1);
-        const uint32_t acc = i > 0 ? 1u : 0u;
         if (one) {
-#pragma unroll
-        for (int m = 0; m < NM; ++m) {
-          if (kQ)
-            mma_from_tmem<W / 16>(tmem + kColX + 64u * m, st + W * m, b1_mn + where(i) + m * kMap,
-                                  id_x, acc);
-          else if (m == 0)
-            mma_from_tmem<W / 16>(tmem + kColX, st, b2_mn + where(i), id_x, acc);
-          mma_from_tmem<W / 16>(tmem + kColY + 64u * m, st + kDP + 8u * m,
-                                b1_mn + where(i) + m * kMap, id_y, acc);
+          issue(0);
+          if (n > 1) issue(1);
         }
-        if ((i + 1) % kHalves == 0) mma_commit(&br.empty[(i / kHalves) % kSlots]);
+        __syncwarp();
+      }
+      // One unit per step: X and Y of step i, then S and dP of step i + 2 into the
+      // stage that they free, behind one round of waits. The issuing lane looks at
+      // the next unit's barriers while this unit's products are in the queue.
+      bool ready = false;
+      for (int i = 0; ok && i < n; ++i) {
+        const bool more = i + 2 < n;
+        const int j = (i + 2) / kHalves;
+        if (!__any_sync(0xFFFFFFFFu, ready)) {
+          ok = mbar_wait(&br.out_full[i & 1], (i >> 1) & 1, abort) &&
+               (!more || mbar_wait(&br.full[j % kSlots], (j / kSlots) & 1, abort));
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+        }
+        tc_fence_after_sync();
+        if (one) {
+          const uint32_t st = tmem + kStage0 + kStage * uint32_t(i & 1);
+          const uint32_t acc = i > 0 ? 1u : 0u;
+#pragma unroll
+          for (int m = 0; m < NM; ++m) {
+            if (kQ)
+              mma_from_tmem<W / 16>(tmem + kColX + 64u * m, st + W * m, b1_mn + where(i) + m * kMap,
+                                    id_x, acc);
+            else if (m == 0)
+              mma_from_tmem<W / 16>(tmem + kColX, st, b2_mn + where(i), id_x, acc);
+            mma_from_tmem<W / 16>(tmem + kColY + 64u * m, st + kDP + 8u * m,
+                                  b1_mn + where(i) + m * kMap, id_y, acc);
+          }
+          if ((i + 1) % kHalves == 0) mma_commit(&br.empty[(i / kHalves) % kSlots]);
+          if (more) issue(i + 2);
+          const int jn = (i + 3) / kHalves;
+          ready = mbar_peek(&br.out_full[(i + 1) & 1], ((i + 1) >> 1) & 1) &&
+                  (i + 3 >= n || mbar_peek(&br.full[jn % kSlots], (jn / kSlots) & 1));
         }
         __syncwarp();
       }
@@ -624,6 +682,16 @@ __global__ void __launch_bounds__(kSbThreads, 1)
       to_h = g.T - g.pt + hp * g.ph;
       to_w = (g.T - g.pt) + (g.Hh - g.ph) + wp * g.pw;
     }
+    float tsum = 0.f;
+    int tcur = to_t;
+    auto flush_t = [&]() {
+      float x = tsum;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+      if (lane == 0) my_hist[tcur - to_t] += x;
+      __syncwarp();
+      tsum = 0.f;
+    };
     const uint32_t st = lane_base + kStage0 + kStage * uint32_t(grp);
     bool ok = true;
     for (int i = grp; i < n; i += 2) {
@@ -667,7 +735,21 @@ __global__ void __launch_bounds__(kSbThreads, 1)
           tmem_ld16(st + kDP + col, dp);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
+          for (int k4 = 0; k4 < 16; k4 += 4) {
+            uint64_t nls[NM][2], nds[NM][2];  // -lse and -D of four columns
+            if (!kQ) {
+#pragma unroll
+              for (int m = 0; m < NM; ++m) {
+                const float4 l = *reinterpret_cast<const float4*>(&sm.nlse[s][m][qcol + k4]);
+                const float4 d = *reinterpret_cast<const float4*>(&sm.ndsum[s][m][qcol + k4]);
+                nls[m][0] = f2_pack(l.x, l.y);
+                nls[m][1] = f2_pack(l.z, l.w);
+                nds[m][0] = f2_pack(d.x, d.y);
+                nds[m][1] = f2_pack(d.z, d.w);
+              }
+            }
+#pragma unroll
+          for (int k = k4; k < k4 + 4; k += 2) {
             const uint64_t e2 = f2_pack(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1]));
             uint64_t p2[NM];
 #pragma unroll
@@ -677,8 +759,8 @@ __global__ void __launch_bounds__(kSbThreads, 1)
                 nl2 = f2_pack(nlse[m], nlse[m]);
                 nd2 = f2_pack(ndsum[m], ndsum[m]);
               } else {
-                nl2 = *reinterpret_cast<const uint64_t*>(&sm.nlse[s][m][qcol + k]);
-                nd2 = *reinterpret_cast<const uint64_t*>(&sm.ndsum[s][m][qcol + k]);
+                nl2 = nls[m][(k - k4) / 2];
+                nd2 = nds[m][(k - k4) / 2];
               }
               if constexpr (!kDiff) {
                 const int q = 16 * ch + k;
@@ -704,6 +786,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
 #pragma unroll
               for (int m = 0; m < NM; ++m) pk[m][k / 2] = f2_bf16(p2[m]);
             }
+          }
           }
         } else {
 #pragma unroll
@@ -733,10 +816,24 @@ __global__ void __launch_bounds__(kSbThreads, 1)
             f2_unpack(gc2[y / 2], lo, hi);
             c[y] = kG == 1 ? lo + hi : (y & 1 ? hi : lo);
           }
-          add_table_grad<L>(my_hist, g, it - to_t, ih - to_h, iw - to_w, wg, lane, f, c);
+          if constexpr (L == 3) {
+            if (g.pt == 1) {
+              if (it != tcur) {  // uniform across the warp
+                flush_t();
+                tcur = it;
+              }
+              tsum += (f[0] + f[1]) + (f[2] + f[3]);
+              add_table_grad_patch(my_hist, ih - to_h, iw - to_w, wg, lane, f, c);
+            } else {
+              add_table_grad<L>(my_hist, g, it - to_t, ih - to_h, iw - to_w, wg, lane, f, c);
+            }
+          } else {
+            add_table_grad<L>(my_hist, g, it - to_t, ih - to_h, iw - to_w, wg, lane, f, c);
+          }
         }
       }
     }
+    if constexpr (kTable && L == 3) flush_t();
     float dfull[NM];
     if (kQ && ok) {
       // D of every row: four warps' partial sums, in a fixed order
@@ -883,6 +980,17 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+// Heads whose tiles are dealt out together, heaviest first: as many as keep q, k,
+// v and dO within 64 MB, half of L2. One head at a time leaves SMs idle behind
+// the last head's heaviest tiles where heads are short (key pass, 12 heads of
+// 8,192 tokens: 424 us in the tiles' own order); all heads at once would stream
+// their blocks from HBM where they are long.
+static int head_group(const Geometry& g) {
+  const size_t head = size_t(4) * g.S * g.d * 2;
+  const size_t n = (size_t(64) << 20) / head;
+  return n < 1 ? 1 : n > size_t(g.BH) ? g.BH : int(n);
+}
+
 template <int D, AttnMode M, int L, bool kQ>
 static cudaError_t launch_pass(const ScoreBwdArgs& a, const Geometry& g, cudaStream_t stream) {
   // the offset tables, and in the key pass the histogram behind them; at least
@@ -898,7 +1006,7 @@ static cudaError_t launch_pass(const ScoreBwdArgs& a, const Geometry& g, cudaStr
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   score_bwd_kernel<D, M, L, kQ>
-      <<<dim3(unsigned(g.ntile), unsigned(g.BH)), kSbThreads, smem, stream>>>(a, g);
+      <<<unsigned(g.ntile) * unsigned(g.BH), kSbThreads, smem, stream>>>(a, g);
   return cudaGetLastError();
 }
 
@@ -922,7 +1030,8 @@ static cudaError_t launch_score_bwd_d(const ScoreBwdArgs& a, const Geometry& g,
   }
 }
 
-cudaError_t launch_score_bwd(const ScoreBwdArgs& a, const Geometry& g, cudaStream_t stream) {
+cudaError_t launch_score_bwd(ScoreBwdArgs a, const Geometry& g, cudaStream_t stream) {
+  a.group = head_group(g);
   const dim3 grid(unsigned((g.S + kPrepRows - 1) / kPrepRows), unsigned(g.BH));
   const bool diff = a.lam != nullptr;
 #define SA_PREP(D, DIFF)                                                                       \
@@ -936,6 +1045,7 @@ cudaError_t launch_score_bwd(const ScoreBwdArgs& a, const Geometry& g, cudaStrea
 #undef SA_PREP
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) e = launch_bwd_lists(a.bits, a.kcnt, a.kidx, g, stream);
+  if (e == cudaSuccess) e = launch_tile_order(a.kcnt, a.korder, g, stream);
   if (e == cudaSuccess)
     e = g.d == 128 ? launch_score_bwd_d<128>(a, g, stream) : launch_score_bwd_d<64>(a, g, stream);
   if (e != cudaSuccess) return e;

@@ -191,6 +191,8 @@ struct ScoreBwdArgs {
   const int32_t* tcnt;
   const int32_t* tidx;
   const int32_t* order;
+  int32_t* korder;  // [BH][ntile]: key tiles of a head, longest list first
+  int group;        // heads dealt out together (set by the launch)
   void* dq;  // [BH][S][d] natural order, bf16 or fp32
   void* dk;
   void* dv;
@@ -204,10 +206,10 @@ struct ScoreBwdArgs {
   int out_fp32;
   int debug_flags;  // SA_DEBUG_STALL_LOADER: the first Q load is never issued (test hook)
 };
-cudaError_t launch_score_bwd(const ScoreBwdArgs& a, const Geometry& g, cudaStream_t stream);
+cudaError_t launch_score_bwd(ScoreBwdArgs a, const Geometry& g, cudaStream_t stream);
 
 struct ScoreBwdLayout {
-  size_t nlse, ndsum, kcnt, kidx, part, total;
+  size_t nlse, ndsum, kcnt, kidx, korder, part, total;
 };
 inline ScoreBwdLayout make_score_bwd_layout(const Geometry& g, int maps, size_t parts_per_head) {
   ScoreBwdLayout b;
@@ -216,6 +218,7 @@ inline ScoreBwdLayout make_score_bwd_layout(const Geometry& g, int maps, size_t 
   b.ndsum = o; o = align256(o + sizeof(float) * maps * size_t(g.BH) * g.S);
   b.kcnt = o; o = align256(o + sizeof(int32_t) * size_t(g.BH) * g.ntile);
   b.kidx = o; o = align256(o + sizeof(int32_t) * size_t(g.BH) * g.ntile * g.nb);
+  b.korder = o; o = align256(o + sizeof(int32_t) * size_t(g.BH) * g.ntile);
   b.part = o; o = align256(o + sizeof(float) * size_t(g.BH) * parts_per_head);
   b.total = o;
   return b;
