@@ -152,8 +152,8 @@ def desc_for(w, out_fp32: bool = False, debug_flags: int = 0) -> SaDesc:
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # (the raw handle: a Stream object takes 3 us to make)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -431,18 +431,18 @@ def _rel_bias(desc: SaDesc, table: torch.Tensor, bucket: torch.Tensor) -> SaRelB
 
 
 def _check_like(name: str, t: torch.Tensor, dtype, shape) -> torch.Tensor:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda or \
-            not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
     return t
 
 
 def _same_device(q: torch.Tensor, *ts: Optional[torch.Tensor]) -> None:
     """Every tensor on q's device, and that device current (its streams are)."""
+    dev = q.get_device()
     for t in ts:
-        if t is not None and t.device != q.device:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"all tensors must be on q's device ({q.device}), got {t.device}")
-    if q.device.index != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         raise ValueError(f"q is on {q.device}, which is not the current device")
 
 
@@ -465,8 +465,10 @@ def fwd_bias(desc: SaDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ta
     _check_qkv(desc, q, k, v)
     want = torch.float32 if desc.out_fp32 else torch.bfloat16
     rel = _rel_bias(desc, table, bucket)
-    out = _check_like("out", _new(q.shape, want, q.device, stream) if out is None else out, want,
-                      q.shape)
+    if out is None:
+        out = _new(q.shape, want, q.device, stream)
+    else:
+        _check_like("out", out, want, q.shape)
     if lse is not None:
         _check_like("lse", lse, torch.float32, q.shape[:3])
     _same_device(q, k, v, table, bucket, workspace, out, lse)
@@ -477,8 +479,8 @@ def fwd_bias(desc: SaDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ta
 
 
 def _grads(q: torch.Tensor, want, given, stream):
-    return [_check_like(n, _new(q.shape, want, q.device, stream) if g is None else g, want, q.shape)
-            for n, g in zip(("dq", "dk", "dv"), given)]
+    return [_new(q.shape, want, q.device, stream) if g is None else
+            _check_like(n, g, want, q.shape) for n, g in zip(("dq", "dk", "dv"), given)]
 
 
 def _score_scratch(desc: SaDesc, size_of, scratch, device, stream) -> torch.Tensor:
@@ -499,8 +501,8 @@ def bwd_bias(desc: SaDesc, q, k, v, table, bucket, out, dout, lse, workspace, dq
     _check_like("out", out, want, q.shape)
     _check_like("lse", lse, torch.float32, q.shape[:3])
     grads = _grads(q, want, (dq, dk, dv), stream)
-    grads.append(_check_like("dtable", _new(table.shape, want, q.device, stream)
-                             if dtable is None else dtable, want, table.shape))
+    grads.append(_new(table.shape, want, q.device, stream) if dtable is None else
+                 _check_like("dtable", dtable, want, table.shape))
     scratch = _score_scratch(desc, lib().sparse_attn_bwd_bias_scratch_size, scratch, q.device, stream)
     _same_device(q, k, v, table, bucket, workspace, out, dout, lse, scratch, *grads)
     _ok(lib().sparse_attn_bwd_bias(ctypes.byref(desc), ctypes.byref(rel), _ptr(q), _ptr(k), _ptr(v),
@@ -524,8 +526,10 @@ def fwd_diff(desc: SaDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, la
     _check_qkv(desc, q, k, v)
     want = torch.float32 if desc.out_fp32 else torch.bfloat16
     _check_lam(desc, lam)
-    out = _check_like("out", _new(q.shape, want, q.device, stream) if out is None else out, want,
-                      q.shape)
+    if out is None:
+        out = _new(q.shape, want, q.device, stream)
+    else:
+        _check_like("out", out, want, q.shape)
     if out2 is not None:
         _check_like("out2", out2, want, q.shape)
     if lse is not None:
@@ -548,8 +552,8 @@ def bwd_diff(desc: SaDesc, q, k, v, lam, out, out2, dout, lse, workspace, dq=Non
     _check_like("out2", out2, want, q.shape)
     _check_like("lse", lse, torch.float32, (2,) + tuple(q.shape[:3]))
     grads = _grads(q, want, (dq, dk, dv), stream)
-    grads.append(_check_like("dlam", _new(lam.shape, want, q.device, stream)
-                             if dlam is None else dlam, want, lam.shape))
+    grads.append(_new(lam.shape, want, q.device, stream) if dlam is None else
+                 _check_like("dlam", dlam, want, lam.shape))
     scratch = _score_scratch(desc, lib().sparse_attn_bwd_diff_scratch_size, scratch, q.device, stream)
     _same_device(q, k, v, lam, workspace, out, out2, dout, lse, scratch, *grads)
     _ok(lib().sparse_attn_bwd_diff(ctypes.byref(desc), _ptr(lam), _ptr(q), _ptr(k), _ptr(v),

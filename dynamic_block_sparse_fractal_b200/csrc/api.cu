@@ -419,8 +419,6 @@ sa_status sparse_attn_plan_mask(const sa_desc* desc, const uint8_t* mask, int ma
   if (st != SA_OK) return st;
   const WsLayout w = make_ws_layout(g);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(at<uint32_t>(workspace, w.status), 0, 256, s) != cudaSuccess)
-    return SA_ERR_CUDA;
   MaskArgs m;
   std::memset(&m, 0, sizeof(m));
   m.bits = at<uint32_t>(workspace, w.bits);
@@ -430,8 +428,7 @@ sa_status sparse_attn_plan_mask(const sa_desc* desc, const uint8_t* mask, int ma
   m.tidx = at<int32_t>(workspace, w.tidx);
   m.status = at<uint32_t>(workspace, w.status);
   const size_t head = mask_heads == 1 ? 0 : size_t(g.nb) * g.nb;
-  if (launch_mask_rows(mask, head, m.bits, m.cnt, m.idx, g, s) != cudaSuccess) return SA_ERR_CUDA;
-  if (launch_union(m, g, s) != cudaSuccess) return SA_ERR_CUDA;
+  if (launch_mask_bytes(m, mask, head, g, s) != cudaSuccess) return SA_ERR_CUDA;
   return cuda_status(launch_tile_order(m.tcnt, at<int32_t>(workspace, w.order), g, s));
 }
 

@@ -91,10 +91,11 @@ constexpr int kMaxList = 2880;
 __host__ __device__ constexpr uint32_t col_s(int x) { return uint32_t(x) * 128u; }
 __host__ __device__ constexpr uint32_t col_o(int x) { return 256u + uint32_t(x) * 128u; }
 
-// What the bias and diff forms keep behind AttnSmem.
-struct DiffSmem {
-  float inv[2][128];  // 1 / l of each map's rows
-  uint64_t inv_full;
+// Behind AttnSmem where A and B belong to one query tile (its two maps, or the
+// two halves of its list): each one's row statistics, met before the outputs join.
+struct JoinSmem {
+  float m[2][128], l[2][128];
+  uint64_t full;
 };
 
 template <int D>
@@ -118,9 +119,11 @@ struct Tile {
   int nsteps;           // ceil(n_u / 2)
   const int32_t* list;   // union entries (shared-memory copy of the first kMaxList)
   const int32_t* glist;  // the same entries in global memory
+  int first;             // the entry that its first step starts at
 };
 
 __device__ __forceinline__ int list_at(const Tile& t, int i) {
+  i += t.first;
   return i < kMaxList ? t.list[i] : __ldg(t.glist + i);
 }
 
@@ -225,8 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr bool kDiff = M == AttnMode::kDiff;
   constexpr bool kBias = M == AttnMode::kBias || M == AttnMode::kBias8;
-  DiffSmem& df = *reinterpret_cast<DiffSmem*>(&sm + 1);   // diff only
-  float* bias = reinterpret_cast<float*>(&sm + 1);        // bias only
+  JoinSmem& join = *reinterpret_cast<JoinSmem*>(&sm + 1);  // bias and diff only
+  float* bias = reinterpret_cast<float*>(&join + 1);       // bias only
+  const bool split = kBias && a.split;  // A and B take half of one tile's list each
+  const bool one_tile = kDiff || split;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y;
   const int pair = blockIdx.x;
@@ -239,9 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     // position in the head's tile order
-    const int pos = kDiff ? pair : 2 * pair + x;
+    const int pos = one_tile ? pair : 2 * pair + x;
     tile[x].qa = tile[x].qb = -1;
-    tile[x].n_u = tile[x].nsteps = 0;
+    tile[x].n_u = tile[x].nsteps = tile[x].first = 0;
     tile[x].list = nullptr;
     tile[x].glist = nullptr;
     if (pos < g.ntile) {
@@ -253,10 +258,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile[x].glist = src;
       // every warp reads the lists at each step: stage them in shared memory
       const int staged = tile[x].n_u < kMaxList ? tile[x].n_u : kMaxList;
-      if (!kDiff || x == 0)
+      if (!one_tile || x == 0)
         for (int i = threadIdx.x; i < staged; i += kThreads) sm.list[x][i] = src[i];
     }
-    tile[x].list = sm.list[kDiff ? 0 : x];
+    tile[x].list = sm.list[one_tile ? 0 : x];
+    if (split) {  // whole steps: A the first half, B the rest
+      const int half = (tile[x].nsteps + 1) / 2;
+      tile[x].first = x == 0 ? 0 : 2 * half;
+      tile[x].n_u = x == 0 ? min(tile[x].n_u, 2 * half) : max(tile[x].n_u - 2 * half, 0);
+      tile[x].nsteps = (tile[x].n_u + 1) >> 1;
+    }
   }
   if constexpr (kBias) relbias_load(bias, a.bias, g, bh, threadIdx.x, kThreads, a.status);
   volatile int* abort = &sm.abort;
@@ -273,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.empty[s], 1);
     }
     mbar_init(&sm.drain, 1);
-    if constexpr (kDiff) mbar_init(&df.inv_full, 256);
+    if constexpr (M != AttnMode::kPlain) mbar_init(&join.full, 256);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&a.map_v2);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (tile[x].nsteps == 0 || (kDiff && x == 1)) continue;
+          if (tile[x].nsteps == 0 || (one_tile && x == 1)) continue;
           mbar_arrive_expect_tx(&sm.q_full[x], 128u * D * 2u);
           for (int e = 0; e < 2; ++e) {
             const int blk = (e == 0 || tile[x].qb < 0) ? tile[x].qa : tile[x].qb;
@@ -394,13 +405,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t kdesc0 = sw128_desc(smem_u32(&sm.slot[0][0][0]), 16, 1024);
       const uint64_t vdesc0 = sw128_desc(smem_u32(&sm.slot[0][0][0]), kChunkBytes, 1024);
       const uint64_t qdesc0 = sw128_desc(smem_u32(&sm.q[0][0][0]), 16, 1024);
-      const uint64_t qdesc1 = sw128_desc(smem_u32(&sm.q[1][0][0]), 16, 1024);
+      const uint64_t qdesc1 = sw128_desc(smem_u32(&sm.q[split ? 0 : 1][0][0]), 16, 1024);
       constexpr uint32_t kSlotStep = (D / 64) * kChunkBytes / 16;  // one slot, 16 B units
       const int u0 = __shfl_sync(0xFFFFFFFFu, tile[0].n_u, 0);
       const int u1 = __shfl_sync(0xFFFFFFFFu, tile[1].n_u, 0);
       const int n0 = (u0 + 1) >> 1, n1 = (u1 + 1) >> 1;
       bool ok = n0 == 0 || mbar_wait(&sm.q_full[0], 0, abort);  // (heaviest first: n1 <= n0)
-      if (!kDiff && ok && n1 > 0) ok = mbar_wait(&sm.q_full[1], 0, abort);
+      if (!one_tile && ok && n1 > 0) ok = mbar_wait(&sm.q_full[1], 0, abort);
       ok = __all_sync(0xFFFFFFFFu, ok);
       int k = 0;  // op index (ring position)
 #if SA_TRACE
@@ -643,12 +654,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       const float inv = l > 0.f ? 1.0f / l : 0.f;
       bool done = t.nsteps == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&sm.o_final[x], 0, abort));
-      if constexpr (kDiff) {
-        // the rows of both maps meet here: 1 / l of each, then both O's in TMEM
-        df.inv[x][r] = inv;
-        mbar_arrive(&df.inv_full);
-        done = done && __all_sync(0xFFFFFFFFu, mbar_wait(&df.inv_full, 0, abort)) &&
-               (t.nsteps == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&sm.o_final[x ^ 1], 0, abort)));
+      const int other = x ? tile[0].nsteps : tile[1].nsteps;
+      if (M != AttnMode::kPlain && one_tile) {
+        // the rows of A and B meet here: their statistics, then both O's in TMEM
+        join.m[x][r] = m;
+        join.l[x][r] = l;
+        mbar_arrive(&join.full);
+        done = done && __all_sync(0xFFFFFFFFu, mbar_wait(&join.full, 0, abort)) &&
+               (other == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&sm.o_final[x ^ 1], 0, abort)));
       }
       if (!done) {
         fail(a.status, &sm.abort, kDevErrTimeoutSoftmax);
@@ -657,23 +670,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t row = size_t(bh) * g.S + block_row_token(g, half ? t.qb : t.qa, r & 63);
         // log-sum-exp of the row's kept scaled scores (natural log): m is
         // in log2 units and l is the sum relative to 2^m
-        if (a.lse != nullptr)
+        const bool two_sums = M != AttnMode::kPlain && split;
+        float w0 = inv, w1 = 0.f;  // what O_A and O_B count in the output
+        if (M != AttnMode::kPlain && one_tile) {
+          const float m0 = join.m[0][r], m1 = join.m[1][r], l0 = join.l[0][r], l1 = join.l[1][r];
+          if constexpr (kDiff) {
+            w0 = l0 > 0.f ? 1.0f / l0 : 0.f;
+            w1 = l1 > 0.f ? 1.0f / l1 : 0.f;
+          } else {
+            // one softmax over both halves: exact, the statistics are fp32
+            const float top = fmaxf(m0, m1);
+            const float e0 = l0 > 0.f ? ex2_approx(m0 - top) : 0.f;
+            const float e1 = l1 > 0.f ? ex2_approx(m1 - top) : 0.f;
+            l = l0 * e0 + l1 * e1;
+            m = top;
+            w0 = l > 0.f ? e0 / l : 0.f;
+            w1 = l > 0.f ? e1 / l : 0.f;
+          }
+        }
+        if (a.lse != nullptr && !(two_sums && x == 1))
           a.lse[row + (kDiff ? size_t(x) * g.BH * g.S : 0)] =
               l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
-        if constexpr (kDiff) {
-          // this map's warps write half of the channels of out and out2
-          const float inv1 = df.inv[0][r], inv2 = df.inv[1][r];
-          const float lam = __bfloat162float(a.lam[bh % a.H]);
+        if (M != AttnMode::kPlain && one_tile) {
+          // A's warps write the first half of the channels, B's the second
+          const float lam = kDiff ? __bfloat162float(a.lam[bh % a.H]) : -1.f;
+          const int na = tile[0].nsteps, nb_ = tile[1].nsteps;
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
             const int col = x * (D / 2) + 32 * c;
             float o1[32], o2[32];
-            load_o32(t_lane + col_o(0) + uint32_t(col), t.nsteps, inv1, o1);
-            load_o32(t_lane + col_o(1) + uint32_t(col), t.nsteps, inv2, o2);
+            load_o32(t_lane + col_o(0) + uint32_t(col), na, w0, o1);
+            load_o32(t_lane + col_o(1) + uint32_t(col), nb_, w1, o2);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o1[i] = fmaf(-lam, o2[i], o1[i]);
             store_o32(a.out, row * D + col, o1, a.out_fp32);
-            if (a.out2 != nullptr) store_o32(a.out2, row * D + col, o2, a.out_fp32);
+            if (kDiff && a.out2 != nullptr) store_o32(a.out2, row * D + col, o2, a.out_fp32);
           }
         } else {
 #pragma unroll
@@ -693,18 +724,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
+// Up to four query tiles per SM, A and B take the halves of one tile's list: twice
+// the CTAs with half the steps each, where pairs of whole tiles leave SMs idle
+// (64 tiles: 37.6 -> 22.6 us; 576: 151 -> 149; 768: 262 -> 266; 3,552: 1,816 ->
+// 1,894, the join and the second prologue of each tile then being pure cost).
+constexpr long kSplitTiles = 4 * 148;
+
 template <int D, AttnMode M>
 static cudaError_t launch_attn_m(const AttnArgs& a, const Geometry& g, cudaStream_t stream) {
   // At least 120 KB so that one CTA occupies an SM: each CTA allocates all
   // 512 TMEM columns.
   size_t need = sizeof(AttnSmem<D>) + 1024;
+  if (M != AttnMode::kPlain) need += sizeof(JoinSmem);
   if (M == AttnMode::kBias || M == AttnMode::kBias8) need += relbias_offsets(g) * sizeof(float);
-  if (M == AttnMode::kDiff) need += sizeof(DiffSmem);
   const size_t smem = need > 120 * 1024 ? need : 120 * 1024;
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, M>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  const dim3 grid(unsigned(M == AttnMode::kDiff ? g.ntile : (g.ntile + 1) / 2), unsigned(g.BH));
+  const bool one_tile = M == AttnMode::kDiff || (M != AttnMode::kPlain && a.split);
+  const dim3 grid(unsigned(one_tile ? g.ntile : (g.ntile + 1) / 2), unsigned(g.BH));
   attn_kernel<D, M><<<grid, kThreads, smem, stream>>>(a, g);
   return cudaGetLastError();
 }
@@ -713,8 +751,10 @@ template <int D>
 static cudaError_t launch_attn_d(const AttnArgs& a, const Geometry& g, cudaStream_t stream) {
   if (a.lam != nullptr) return launch_attn_m<D, AttnMode::kDiff>(a, g, stream);
   if (a.bias.table == nullptr) return launch_attn_m<D, AttnMode::kPlain>(a, g, stream);
-  return g.lpw == 3 ? launch_attn_m<D, AttnMode::kBias8>(a, g, stream)
-                    : launch_attn_m<D, AttnMode::kBias>(a, g, stream);
+  AttnArgs b = a;
+  b.split = long(g.ntile) * g.BH <= kSplitTiles;
+  return g.lpw == 3 ? launch_attn_m<D, AttnMode::kBias8>(b, g, stream)
+                    : launch_attn_m<D, AttnMode::kBias>(b, g, stream);
 }
 
 cudaError_t launch_attn(const AttnArgs& a, const Geometry& g, cudaStream_t stream) {

@@ -765,7 +765,45 @@ SA_HD int union_words_per_warp(const Geometry& g) {
   return 2 * (bitmap_words(g) + 1) + 2 * g.nt * fw;
 }
 
-__global__ void __launch_bounds__(kUnionMaxWarps * 32) union_kernel(MaskArgs a, Geometry g) {
+// One q-block row of a caller's byte mask, by one warp: the keep bitmap (global
+// and shared copy), count and ascending list, as the select step writes them. A
+// word of the bitmap per ballot, four words' loads in flight.
+__device__ __forceinline__ void byte_row(const MaskArgs& a, const Geometry& g, const uint8_t* mask,
+                                         size_t head_stride, int bh, int qb, uint32_t* shared) {
+  const int lane = threadIdx.x & 31, nwords = bitmap_words(g);
+  const size_t row = size_t(bh) * g.nb + qb;
+  const uint8_t* src = mask + size_t(bh) * head_stride + size_t(qb) * g.nb;
+  uint32_t* bits = a.bits + row * nwords;
+  int32_t* out = a.idx + row * g.nb;
+  int n = 0;
+  for (int w0 = 0; w0 < nwords; w0 += 4) {
+    uint8_t x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = 32 * (w0 + u) + lane;
+      x[u] = j < g.nb ? __ldg(src + j) : uint8_t(0);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (w0 + u >= nwords) break;
+      const unsigned m = __ballot_sync(kFull, x[u] != 0);
+      if (x[u] != 0) out[n + __popc(m & lanemask_lt())] = 32 * (w0 + u) + lane;
+      if (lane == 0) bits[w0 + u] = shared[w0 + u] = m;
+      n += __popc(m);
+    }
+  }
+  if (lane == 0) {
+    a.cnt[row] = n;
+    shared[nwords] = 0u;
+  }
+}
+
+// kBytes: the rows come from a caller's byte mask (this kernel is then the whole
+// plan but the tile order: one launch in place of three, 5 us of a small call's
+// time), otherwise from the bitmaps of the select or radius step.
+template <bool kBytes>
+__global__ void __launch_bounds__(kUnionMaxWarps * 32)
+    union_kernel(MaskArgs a, const uint8_t* __restrict__ mask, size_t head_stride, Geometry g) {
   extern __shared__ uint32_t ush[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nwords = bitmap_words(g);
@@ -781,9 +819,19 @@ __global__ void __launch_bounds__(kUnionMaxWarps * 32) union_kernel(MaskArgs a, 
   uint32_t* ub = ua + nwords + 1;
   uint32_t* firstF = ub + nwords + 1;
   uint32_t* leftF = firstF + nf;
-  for (int w = lane; w <= nwords; w += 32) {
-    ua[w] = w < nwords ? ba[w] : 0u;
-    ub[w] = (bb != nullptr && w < nwords) ? bb[w] : 0u;
+  if constexpr (kBytes) {
+    if (item == 0 && lane == 0) *a.status = 0u;
+    byte_row(a, g, mask, head_stride, bh, qa, ua);
+    if (qb >= 0) {
+      byte_row(a, g, mask, head_stride, bh, qb, ub);
+    } else {
+      for (int w = lane; w <= nwords; w += 32) ub[w] = 0u;
+    }
+  } else {
+    for (int w = lane; w <= nwords; w += 32) {
+      ua[w] = w < nwords ? ba[w] : 0u;
+      ub[w] = (bb != nullptr && w < nwords) ? bb[w] : 0u;
+    }
   }
   __syncwarp();
 
@@ -935,14 +983,25 @@ cudaError_t launch_mask(const MaskArgs& a, const Geometry& g, cudaStream_t strea
   return launch_union(a, g, stream);
 }
 
-cudaError_t launch_union(const MaskArgs& a, const Geometry& g, cudaStream_t stream) {
+template <bool kBytes>
+static cudaError_t launch_union_of(const MaskArgs& a, const uint8_t* mask, size_t head_stride,
+                                   const Geometry& g, cudaStream_t stream) {
   const long items = long(g.BH) * g.ntile;
   const size_t warp_bytes = size_t(union_words_per_warp(g)) * sizeof(uint32_t);
   int wpc = int((48 * 1024) / warp_bytes);  // warps per CTA within 48 KB
   wpc = wpc < 1 ? 1 : (wpc > kUnionMaxWarps ? kUnionMaxWarps : wpc);
-  union_kernel<<<unsigned((items + wpc - 1) / wpc), unsigned(wpc * 32), wpc * warp_bytes,
-                 stream>>>(a, g);
+  union_kernel<kBytes><<<unsigned((items + wpc - 1) / wpc), unsigned(wpc * 32), wpc * warp_bytes,
+                         stream>>>(a, mask, head_stride, g);
   return cudaGetLastError();
+}
+
+cudaError_t launch_union(const MaskArgs& a, const Geometry& g, cudaStream_t stream) {
+  return launch_union_of<false>(a, nullptr, 0, g, stream);
+}
+
+cudaError_t launch_mask_bytes(const MaskArgs& a, const uint8_t* mask, size_t head_stride,
+                              const Geometry& g, cudaStream_t stream) {
+  return launch_union_of<true>(a, mask, head_stride, g, stream);
 }
 
 // One CTA per head: bitonic sort of the head's tiles by descending union

@@ -363,9 +363,9 @@ static_assert(sizeof(SbSmem<128, 4>) + 1024 + sizeof(float) * (2 * kRelBiasMaxAx
 }  // namespace
 
 // -D_m and -lse_m * log2(e) of every row into fractal order (negated: both are
-// addends; an empty row's lse = -inf stays -inf, so that 2^(z - lse) is 0). D/8 lanes per row, 128 rows
+// addends; an empty row's lse = -inf stays -inf, so that 2^(z - lse) is 0). D/8 lanes per row, 32 rows
 // per CTA, one head per CTA.
-constexpr int kPrepRows = 128;
+constexpr int kPrepRows = 32;
 
 template <int D, bool kDiff>
 __global__ void __launch_bounds__(256)
@@ -464,7 +464,9 @@ __global__ void __launch_bounds__(kSbThreads, 1)
   const int heads = min(a.group, g.BH - first_head);
   const int in_group = int(blockIdx.x) - first_head * g.ntile;
   const int bh = first_head + in_group % heads;
-  const int tile = (kQ ? a.order : a.korder)[size_t(bh) * g.ntile + in_group / heads];
+  const int32_t* order = kQ ? a.order : a.korder;
+  const int tile = order == nullptr ? in_group / heads
+                                    : order[size_t(bh) * g.ntile + in_group / heads];
   int ba, bb;  // the tile's blocks (bb = -1: a lone block)
   tile_blocks(g, tile, ba, bb);
   const size_t unit = size_t(bh) * g.ntile + tile;
@@ -910,42 +912,49 @@ __global__ void __launch_bounds__(kSbThreads, 1)
 }
 
 // dtable: per head, the tiles' partial sums over offsets (part [BH][ntile][noff])
-// added over batch and tiles in a fixed order, 32 offsets x 32 groups of tiles
-// at a time, then over the offsets of each bucket. One CTA per head.
+// added over batch and tiles, a group of threads per share of the tiles, then over
+// the offsets of each bucket, a warp per bucket; all in a fixed order. One CTA per
+// head.
 __global__ void __launch_bounds__(1024)
     dtable_kernel(const float* __restrict__ part, BiasArgs b, int B, void* __restrict__ dtable,
                   int fp32, Geometry g) {
-  __shared__ float sums[2 * kRelBiasMaxAxes], red[32][33];
-  const int h = blockIdx.x, lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  __shared__ float sums[2 * kRelBiasMaxAxes], red[1024];
+  const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int noff = relbias_offsets(g);
-  for (int o0 = 0; o0 < noff; o0 += 32) {
-    const int o = o0 + lane;
+  for (int o0 = 0; o0 < noff; o0 += 1024) {
+    const int here = min(noff - o0, 1024), groups = 1024 / here;
+    const int grp = threadIdx.x / here, o = threadIdx.x - grp * here;
     float s = 0.f;
-    if (o < noff) {
+    if (grp < groups) {
       for (int e = 0; e < B; ++e) {
-        const float* src = part + (size_t(e) * b.H + h) * g.ntile * noff + o;
-#pragma unroll 4
-        for (int t = grp; t < g.ntile; t += 32) s += src[size_t(t) * noff];
+        const float* src = part + (size_t(e) * b.H + h) * g.ntile * noff + o0 + o;
+#pragma unroll 8
+        for (int t = grp; t < g.ntile; t += groups) s += src[size_t(t) * noff];
       }
+      red[threadIdx.x] = s;
     }
-    red[grp][lane] = s;
     __syncthreads();
-    float x = red[lane][grp];  // group `lane` of offset o0 + grp
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, k);
-    if (lane == 0 && o0 + grp < noff) sums[o0 + grp] = x;
+    if (int(threadIdx.x) < here) {
+      s = 0.f;
+      for (int k = 0; k < groups; ++k) s += red[k * here + threadIdx.x];
+      sums[o0 + threadIdx.x] = s;
+    }
     __syncthreads();
   }
-  for (int k = threadIdx.x; k < b.n_buckets; k += blockDim.x) {
+  for (int k = warp; k < b.n_buckets; k += 32) {
     float s = 0.f;
-    for (int i = 0; i < noff; ++i) {
+    for (int i = lane; i < noff; i += 32) {
       int bk = __ldg(b.bucket + i);
       if (bk < 0 || bk >= b.n_buckets) bk = 0;  // as the kernels read it
       if (bk == k) s += sums[i];
     }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
     const size_t at = size_t(h) * b.n_buckets + k;
-    if (fp32) static_cast<float*>(dtable)[at] = s;
-    else static_cast<__nv_bfloat16*>(dtable)[at] = __float2bfloat16_rn(s);
+    if (lane == 0) {
+      if (fp32) static_cast<float*>(dtable)[at] = s;
+      else static_cast<__nv_bfloat16*>(dtable)[at] = __float2bfloat16_rn(s);
+    }
   }
 }
 
@@ -1045,7 +1054,9 @@ cudaError_t launch_score_bwd(ScoreBwdArgs a, const Geometry& g, cudaStream_t str
 #undef SA_PREP
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) e = launch_bwd_lists(a.bits, a.kcnt, a.kidx, g, stream);
-  if (e == cudaSuccess) e = launch_tile_order(a.kcnt, a.korder, g, stream);
+  // (no order where every key tile starts at once)
+  if (long(g.ntile) * g.BH <= 148) a.korder = nullptr;
+  else if (e == cudaSuccess) e = launch_tile_order(a.kcnt, a.korder, g, stream);
   if (e == cudaSuccess)
     e = g.d == 128 ? launch_score_bwd_d<128>(a, g, stream) : launch_score_bwd_d<64>(a, g, stream);
   if (e != cudaSuccess) return e;

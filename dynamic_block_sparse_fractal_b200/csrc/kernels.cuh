@@ -64,9 +64,10 @@ cudaError_t launch_radius(const RadiusArgs& a, const Geometry& g, cudaStream_t s
 bool radius_supported(const Geometry& g);
 
 // The caller's block mask (bytes, 0 = dropped; [BH][nb][nb], or one [nb][nb]
-// for all heads when head_stride is 0) as bitmaps, counts and ascending lists.
-cudaError_t launch_mask_rows(const uint8_t* mask, size_t head_stride, uint32_t* bits, int32_t* cnt,
-                             int32_t* idx, const Geometry& g, cudaStream_t stream);
+// for all heads when head_stride is 0) as bitmaps, counts, ascending lists and
+// per-tile union lists (a's fields of these names); clears a.status.
+cudaError_t launch_mask_bytes(const MaskArgs& a, const uint8_t* mask, size_t head_stride,
+                              const Geometry& g, cudaStream_t stream);
 
 // Per head: tiles sorted by descending union length (ties by tile index).
 cudaError_t launch_tile_order(const int32_t* tcnt, int32_t* order, const Geometry& g,
@@ -105,6 +106,7 @@ struct AttnArgs {
   float* lse;  // [BH][S] natural order: each row's log-sum-exp (natural log), or null
                // (differential: [2][BH][S], one per map)
   BiasArgs bias;             // relative position bias, or a null table
+  bool split;                // bias: one query tile per CTA, its list in two halves (set by the launch)
   const __nv_bfloat16* lam;  // differential: [H] weights of the second map, or null
   void* out2;                // differential: P_2 V [BH][S][d] like out, or null
   int H;                     // differential: heads (bh % H picks lam's entry)
