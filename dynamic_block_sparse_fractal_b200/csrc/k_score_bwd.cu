@@ -20,10 +20,14 @@
 //
 // D. rowsum(dO * O) of a stored bf16 output carries its rounding, and the error
 // of D is common to a whole row of dS. The query pass therefore starts from that
-// value D~ (dS~ = P (dP - D~)), sums D = rowsum(P * dP) in fp32 on the way, and
-// corrects dQ = dS~ K - (D - D~) P K at the end with one more product, P K; the
-// key pass reads the corrected D. (With D~ alone dQ was 4.5e-3 off in the 2-norm
-// and the parameters' gradients up to 7e-3.)
+// value D~ (dS~ = P (dP - D~)) and sums D = rowsum(P * dP) in fp32 on the way; the
+// key pass reads that D. For dQ one more product, P K, sets a row right: a row of
+// dS sums to 0, so with R = the sum of the row's dS~ as rounded to bf16, dQ = dS~ K
+// - R P K. That takes out D~'s error and the part of the roundings that lies along
+// the row's mean key, which is the largest where keys share a component. (2-norm
+// error of dQ against 64 bits, bf16 outputs: 4.5e-3 with D~ alone, 2.9e-3 with D,
+// 2.3e-3 with R; the bf16 rounding of dQ itself is 1.7e-3. Gradients of the table
+// and of lambda: up to 7e-3 with D~, 2e-3 with D.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -343,10 +347,10 @@ struct __align__(1024) SbSmem {
   uint8_t ta[D / 64][kTile], tb[D / 64][kTile];               // the tile's K, V (or Q, dO)
   uint8_t sa[kSlots][D / 64][kBlk], sb[kSlots][D / 64][kBlk];  // streamed Q, dO (or K, V)
   float nlse[kSbSlots][2][64], ndsum[kSbSlots][2][64];        // of streamed query rows, per map
+  float sums[2][2][4][128];  // query pass: four warps' parts of a row's D and R, per map
   int32_t list[kSbList];
   SbBars bar;
 };
-// (the query pass sums each row's D over four warps in the statistics' place)
 // Floats of one row warp's histogram: the offsets between a token of one block
 // and any token, per axis.
 SA_HD int hist_floats(const Geometry& g) {
@@ -664,12 +668,12 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     const uint64_t nlam2 = f2_pack(-lam, -lam);
     const size_t my_pos = size_t(bh) * g.S + size_t(blk) * 64 + (r & 63);
     float nlse[NM], ndsum[NM];  // query pass: this row's
-    uint64_t dfull2[NM];
+    uint64_t dfull2[NM], rsum2[NM];  // sums of P dP, and of dS as rounded
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       nlse[m] = kQ ? a.nlse[size_t(m) * g.BH * g.S + my_pos] : 0.f;
       ndsum[m] = kQ ? a.ndsum[size_t(m) * g.BH * g.S + my_pos] : 0.f;
-      dfull2[m] = 0ull;
+      dfull2[m] = rsum2[m] = 0ull;
     }
     constexpr int kSign = kQ ? 1 : -1;
     constexpr int kG = Cols<L>::kG, kF = Cols<L>::kF;
@@ -775,7 +779,11 @@ __global__ void __launch_bounds__(kSbThreads, 1)
               if (kQ) dfull2[m] = f2_fma(p2[m], e2, dfull2[m]);
               // (map 2: -lambda is applied to the finished dQ_2 and dK_2)
               const uint64_t d2 = f2_mul(p2[m], f2_add(e2, nd2));
-              ds[m][k / 2] = f2_bf16(d2);
+              const uint32_t d16 = f2_bf16(d2);
+              ds[m][k / 2] = d16;
+              if (kQ)
+                rsum2[m] = f2_add(rsum2[m], f2_pack(__uint_as_float(d16 << 16),
+                                                    __uint_as_float(d16 & 0xFFFF0000u)));
               if constexpr (kTable) {
                 const int q = 16 * ch + k;
                 gf2[kG > 1 ? q / kG : q / 2] = f2_add(gf2[kG > 1 ? q / kG : q / 2], d2);
@@ -836,19 +844,23 @@ __global__ void __launch_bounds__(kSbThreads, 1)
       }
     }
     if constexpr (kTable && L == 3) flush_t();
-    float dfull[NM];
+    float dfull[NM], rsum[NM];
     if (kQ && ok) {
-      // D of every row: four warps' partial sums, in a fixed order
-      float* sums = &sm.nlse[0][0][0];  // [map][part][row]
+      // four warps' partial sums of every row, in a fixed order
 #pragma unroll
-      for (int m = 0; m < NM; ++m) sums[(m * 4 + part) * 128 + r] = f2_sum(dfull2[m]);
+      for (int m = 0; m < NM; ++m) {
+        sm.sums[0][m][part][r] = f2_sum(dfull2[m]);
+        sm.sums[1][m][part][r] = f2_sum(rsum2[m]);
+      }
       warp_arrive(&br.dsum_full, lane);
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&br.dsum_full, 0, abort));
       if (ok) {
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-          const float* x = sums + m * 512 + r;
-          dfull[m] = (x[0] + x[128]) + (x[256] + x[384]);
+          const auto& d = sm.sums[0][m];
+          const auto& x = sm.sums[1][m];
+          dfull[m] = (d[0][r] + d[1][r]) + (d[2][r] + d[3][r]);
+          rsum[m] = (x[0][r] + x[1][r]) + (x[2][r] + x[3][r]);
         }
       }
     }
@@ -870,7 +882,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
           const bool second = kDiff && c >= D / 2;
           const float mul = second ? -lam * a.scale : a.scale;  // dS_2 = -lambda P_2 (dP - D_2)
           if constexpr (kQ) {
-            const float fix = second ? dfull[NM - 1] + ndsum[NM - 1] : dfull[0] + ndsum[0];
+            const float fix = second ? rsum[NM - 1] : rsum[0];
             store_acc32<true>(y, lane_base + kColX + acc_col<D, kDiff>(c), n > 0, mul, fix, a.dq, dst,
                         a.out_fp32);
           } else {

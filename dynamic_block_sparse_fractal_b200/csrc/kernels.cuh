@@ -82,9 +82,9 @@ enum class AttnMode { kPlain, kBias, kBias8, kDiff };
 // through bucket[], the table index of every offset along t, then h, then w
 // ((2T-1) + (2Hh-1) + (2Ww-1) entries, offset key - query, lowest first).
 // Offsets along the three axes, and the most that the kernels' shared memory
-// holds (T + Hh + Ww <= 640).
+// holds (T + Hh + Ww <= 512).
 SA_HD int relbias_offsets(const Geometry& g) { return 2 * (g.T + g.Hh + g.Ww) - 3; }
-constexpr int kRelBiasMaxAxes = 640;
+constexpr int kRelBiasMaxAxes = 512;
 struct BiasArgs {
   const __nv_bfloat16* table;  // null: no bias
   const int32_t* bucket;

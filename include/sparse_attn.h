@@ -459,7 +459,7 @@ typedef struct sa_rel_bias {
 
 /* sparse_attn_fwd with the bias. lse (may be NULL): as for sparse_attn_fwd_lse,
  * of the biased scores. The workspace holds any plan made for the same desc.
- * SA_ERR_UNSUPPORTED when T + Hh + Ww > 640. A row whose kept offsets are all
+ * SA_ERR_UNSUPPORTED when T + Hh + Ww > 512. A row whose kept offsets are all
  * masked is treated as one that keeps nothing. */
 sa_status sparse_attn_fwd_bias(const sa_desc* desc, const sa_rel_bias* bias, const void* q,
                                const void* k, const void* v, const void* workspace,

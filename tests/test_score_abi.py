@@ -74,8 +74,8 @@ def test_bias_refusals():
     n = ctypes.c_size_t(0)
     assert api.lib().sparse_attn_bwd_bias_scratch_size(ctypes.byref(d), ctypes.byref(n)) == api.SA_OK
     assert bwd_bias(d, rel(), ssize=n.value - 1) == api.SA_ERR_WORKSPACE
-    # the offset tables' limit: T + Hh + Ww <= 640
-    long = desc(T=632)
+    # the offset tables' limit: T + Hh + Ww <= 512
+    long = desc(T=500)
     assert fwd_bias(long, rel()) == api.SA_ERR_UNSUPPORTED
     assert bwd_bias(long, rel()) == api.SA_ERR_UNSUPPORTED
 
