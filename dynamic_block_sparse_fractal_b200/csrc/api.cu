@@ -181,13 +181,6 @@ const char* sparse_attn_plan_stage_name(int i) {
   return (i >= 0 && i < kNumPlanStages) ? kPlanStages[i] : nullptr;
 }
 
-// What the score functions other than q.k alone add to the attention call.
-struct Score {
-  BiasArgs bias;              // null table: none
-  const __nv_bfloat16* lam;   // differential: weights of the second map
-  void* out2;
-};
-
 // Arguments of a relative position bias; *args and the offset tables' limits.
 static sa_status check_bias(const sa_desc* desc, const sa_rel_bias* b, BiasArgs* args) {
   if (b == nullptr || b->table == nullptr || b->bucket == nullptr || !aligned(b->table, 2) ||
@@ -200,7 +193,7 @@ static sa_status check_bias(const sa_desc* desc, const sa_rel_bias* b, BiasArgs*
 
 static sa_status fwd_impl(const sa_desc* desc, const void* q, const void* k, const void* v,
                           const void* workspace, size_t ws_bytes, void* out, float* lse,
-                          void* stream, const Score* score = nullptr) {
+                          void* stream) {
   sa_status st = validate(desc);
   if (st != SA_OK) return st;
   if (q == nullptr || k == nullptr || v == nullptr || out == nullptr || !aligned(q, 16) ||
@@ -228,14 +221,6 @@ static sa_status fwd_impl(const sa_desc* desc, const void* q, const void* k, con
   a.out_fp32 = desc->out_fp32;
   a.debug_flags = desc->debug_flags;
   a.lse = lse;
-  if (score != nullptr) {
-    a.bias = score->bias;
-    a.lam = score->lam;
-    a.out2 = score->out2;
-    a.H = desc->H;
-    if (a.lam != nullptr)
-      a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)(g.d / 2)));
-  }
   return cuda_status(launch_attn(a, g, static_cast<cudaStream_t>(stream)));
 }
 
@@ -432,28 +417,60 @@ sa_status sparse_attn_plan_mask(const sa_desc* desc, const uint8_t* mask, int ma
   return cuda_status(launch_tile_order(m.tcnt, at<int32_t>(workspace, w.order), g, s));
 }
 
+// The forward with a bias, or of differential attention (lambda given).
+static sa_status score_fwd_impl(const sa_desc* desc, const BiasArgs& bias, const void* lambda,
+                                const void* q, const void* k, const void* v, const void* workspace,
+                                size_t ws_bytes, void* out, void* out2, float* lse, void* stream) {
+  if (q == nullptr || k == nullptr || v == nullptr || out == nullptr || !aligned(q, 16) ||
+      !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+      (out2 != nullptr && !aligned(out2, 16)) || (lse != nullptr && !aligned(lse, 4)))
+    return SA_ERR_INVALID_ARG;
+  const Geometry g = make_geometry(*desc);
+  const sa_status st = check_ws(g, workspace, ws_bytes);
+  if (st != SA_OK) return st;
+  const WsLayout w = make_ws_layout(g);
+  ScoreFwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (!encode_tile_map(&a.map_q, q, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
+      !encode_tile_map(&a.map_k, k, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
+      !encode_tile_map(&a.map_v, v, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw))
+    return SA_ERR_CUDA;
+  a.out = out;
+  a.out2 = out2;
+  a.lse = lse;
+  a.tcnt = at<int32_t>(workspace, w.tcnt);
+  a.tidx = at<int32_t>(workspace, w.tidx);
+  a.order = at<int32_t>(workspace, w.order);
+  a.bias = bias;
+  a.lam = static_cast<const __nv_bfloat16*>(lambda);
+  a.H = desc->H;
+  a.status = const_cast<uint32_t*>(at<uint32_t>(workspace, w.status));
+  a.scale_log2 =
+      (float)(1.4426950408889634 / std::sqrt((double)(lambda != nullptr ? g.d / 2 : g.d)));
+  a.out_fp32 = desc->out_fp32;
+  a.debug_flags = desc->debug_flags;
+  return cuda_status(launch_score_fwd(a, g, static_cast<cudaStream_t>(stream)));
+}
+
 sa_status sparse_attn_fwd_bias(const sa_desc* desc, const sa_rel_bias* bias, const void* q,
                                const void* k, const void* v, const void* workspace,
                                size_t ws_bytes, void* out, float* lse, void* stream) {
   sa_status st = validate(desc);
   if (st != SA_OK) return st;
-  Score sc = {};
-  st = check_bias(desc, bias, &sc.bias);
+  BiasArgs b;
+  st = check_bias(desc, bias, &b);
   if (st != SA_OK) return st;
-  if (lse != nullptr && !aligned(lse, 4)) return SA_ERR_INVALID_ARG;
-  return fwd_impl(desc, q, k, v, workspace, ws_bytes, out, lse, stream, &sc);
+  return score_fwd_impl(desc, b, nullptr, q, k, v, workspace, ws_bytes, out, nullptr, lse, stream);
 }
 
 sa_status sparse_attn_fwd_diff(const sa_desc* desc, const void* lambda, const void* q,
                                const void* k, const void* v, const void* workspace,
                                size_t ws_bytes, void* out, void* out2, float* lse, void* stream) {
-  if (lambda == nullptr || !aligned(lambda, 2) || (out2 != nullptr && !aligned(out2, 16)) ||
-      (lse != nullptr && !aligned(lse, 4)))
-    return SA_ERR_INVALID_ARG;
-  Score sc = {};
-  sc.lam = static_cast<const __nv_bfloat16*>(lambda);
-  sc.out2 = out2;
-  return fwd_impl(desc, q, k, v, workspace, ws_bytes, out, lse, stream, &sc);
+  const sa_status st = validate(desc);
+  if (st != SA_OK) return st;
+  if (lambda == nullptr || !aligned(lambda, 2)) return SA_ERR_INVALID_ARG;
+  return score_fwd_impl(desc, BiasArgs{}, lambda, q, k, v, workspace, ws_bytes, out, out2, lse,
+                        stream);
 }
 
 // Scratch of the gradients of either score function.

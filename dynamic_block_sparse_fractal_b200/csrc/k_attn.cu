@@ -34,16 +34,8 @@
 // when the softmax of tile X sees S_X(j) complete, PV_X(j-1) (issued before
 // S_X(j)) is complete too, and O_X may be rescaled without another wait.
 //
-// Two more forms of the same kernel (template parameter M):
-//   bias  s gets a learned relative position bias before the softmax: the head's
-//         three offset tables (log2 units) lie in shared memory, and a thread
-//         adds one value per key row and one per key column of the block.
-//   diff  differential attention, O = P_1 V - lambda P_2 V: tiles A and B are
-//         the two maps of ONE query tile (channels [0, d/2) and [d/2, d) of q
-//         and k), so S_X takes K = d/2 and both maps run the same list; the
-//         epilogue joins O_A and O_B in TMEM, half of the columns per map's warps.
-// A tile whose rows keep nothing (only a caller's own mask has such) writes
-// zeros and a log-sum-exp of -inf.
+// A tile whose rows keep nothing (only a caller's own mask has such) writes zeros
+// and a log-sum-exp of -inf.
 //
 // All waits are bounded (sm100.cuh); a wait that runs out records a status
 // bit, raises a CTA-wide abort flag, drains its own in-flight work and lets
@@ -53,7 +45,6 @@
 
 #include "exp2_poly.cuh"
 #include "kernels.cuh"
-#include "relbias.cuh"
 #include "sm100.cuh"
 
 namespace sa {
@@ -91,13 +82,6 @@ constexpr int kMaxList = 2880;
 __host__ __device__ constexpr uint32_t col_s(int x) { return uint32_t(x) * 128u; }
 __host__ __device__ constexpr uint32_t col_o(int x) { return 256u + uint32_t(x) * 128u; }
 
-// Behind AttnSmem where A and B belong to one query tile (its two maps, or the
-// two halves of its list): each one's row statistics, met before the outputs join.
-struct JoinSmem {
-  float m[2][128], l[2][128];
-  uint64_t full;
-};
-
 template <int D>
 struct __align__(1024) AttnSmem {
   uint8_t q[2][D / 64][kChunkBytes];
@@ -119,11 +103,9 @@ struct Tile {
   int nsteps;           // ceil(n_u / 2)
   const int32_t* list;   // union entries (shared-memory copy of the first kMaxList)
   const int32_t* glist;  // the same entries in global memory
-  int first;             // the entry that its first step starts at
 };
 
 __device__ __forceinline__ int list_at(const Tile& t, int i) {
-  i += t.first;
   return i < kMaxList ? t.list[i] : __ldg(t.glist + i);
 }
 
@@ -182,56 +164,18 @@ __device__ __forceinline__ int s_op_index(int x, int step, int n0, int n1) {
   return x == 0 ? base + 1 : base + (i < n0) + (i + 1 < n0) + 1;
 }
 
-// 32 columns of O times `inv`, or zeros when the tile ran no step.
-__device__ __forceinline__ void load_o32(uint32_t col, int nsteps, float inv, float (&x)[32]) {
-  if (nsteps > 0) {
-    uint32_t o[32];
-    tmem_ld32(col, o);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * inv;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = 0.f;
-  }
-}
-
-// 32 values -> elements [at, at + 32) of an output, bf16 or fp32.
-__device__ __forceinline__ void store_o32(void* out, size_t at, const float (&x)[32], int fp32) {
-  if (fp32) {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-    for (int v = 0; v < 8; ++v)
-      dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
-  } else {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at);
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-      dst[v] = make_uint4(pack_bf16x2(x[8 * v], x[8 * v + 1]),
-                          pack_bf16x2(x[8 * v + 2], x[8 * v + 3]),
-                          pack_bf16x2(x[8 * v + 4], x[8 * v + 5]),
-                          pack_bf16x2(x[8 * v + 6], x[8 * v + 7]));
-  }
-}
-
 __device__ __forceinline__ int step_blocks(const Tile& t, int step) {
   return (t.n_u - 2 * step) >= 2 ? 2 : 1;
 }
 
 }  // namespace
 
-template <int D, AttnMode M>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ AttnArgs a, const Geometry g) {
   extern __shared__ uint8_t smem_raw[];
   AttnSmem<D>& sm = *reinterpret_cast<AttnSmem<D>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr bool kDiff = M == AttnMode::kDiff;
-  constexpr bool kBias = M == AttnMode::kBias || M == AttnMode::kBias8;
-  JoinSmem& join = *reinterpret_cast<JoinSmem*>(&sm + 1);  // bias and diff only
-  float* bias = reinterpret_cast<float*>(&join + 1);       // bias only
-  const bool split = kBias && a.split;  // A and B take half of one tile's list each
-  const bool one_tile = kDiff || split;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y;
   const int pair = blockIdx.x;
@@ -243,10 +187,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   Tile tile[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    // position in the head's tile order
-    const int pos = one_tile ? pair : 2 * pair + x;
+    const int pos = 2 * pair + x;  // position in the head's tile order
     tile[x].qa = tile[x].qb = -1;
-    tile[x].n_u = tile[x].nsteps = tile[x].first = 0;
+    tile[x].n_u = tile[x].nsteps = 0;
     tile[x].list = nullptr;
     tile[x].glist = nullptr;
     if (pos < g.ntile) {
@@ -258,18 +201,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile[x].glist = src;
       // every warp reads the lists at each step: stage them in shared memory
       const int staged = tile[x].n_u < kMaxList ? tile[x].n_u : kMaxList;
-      if (!one_tile || x == 0)
-        for (int i = threadIdx.x; i < staged; i += kThreads) sm.list[x][i] = src[i];
+      for (int i = threadIdx.x; i < staged; i += kThreads) sm.list[x][i] = src[i];
     }
-    tile[x].list = sm.list[one_tile ? 0 : x];
-    if (split) {  // whole steps: A the first half, B the rest
-      const int half = (tile[x].nsteps + 1) / 2;
-      tile[x].first = x == 0 ? 0 : 2 * half;
-      tile[x].n_u = x == 0 ? min(tile[x].n_u, 2 * half) : max(tile[x].n_u - 2 * half, 0);
-      tile[x].nsteps = (tile[x].n_u + 1) >> 1;
-    }
+    tile[x].list = sm.list[x];
   }
-  if constexpr (kBias) relbias_load(bias, a.bias, g, bh, threadIdx.x, kThreads, a.status);
   volatile int* abort = &sm.abort;
 
   if (threadIdx.x == 0) {
@@ -284,7 +219,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.empty[s], 1);
     }
     mbar_init(&sm.drain, 1);
-    if constexpr (M != AttnMode::kPlain) mbar_init(&join.full, 256);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -315,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&a.map_v2);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (tile[x].nsteps == 0 || (one_tile && x == 1)) continue;
+          if (tile[x].nsteps == 0) continue;
           mbar_arrive_expect_tx(&sm.q_full[x], 128u * D * 2u);
           for (int e = 0; e < 2; ++e) {
             const int blk = (e == 0 || tile[x].qb < 0) ? tile[x].qa : tile[x].qb;
@@ -346,17 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const Tile t = x ? tile[1] : tile[0];
         const int nblk = step_blocks(t, step);
-        // channel chunks of the op: a differential map's S needs its own half
-        const bool half_k = kDiff && D == 128 && kind == 0;
-        const int c_lo = half_k ? x : 0, c_hi = half_k ? x + 1 : D / 64;
-        mbar_arrive_expect_tx(&sm.full[s], uint32_t(nblk) * 64u * uint32_t(c_hi - c_lo) * 128u);
+        mbar_arrive_expect_tx(&sm.full[s], uint32_t(nblk) * 64u * D * 2u);
         const int e0 = list_at(t, 2 * step);
         if (nblk == 2 && (e0 & kEntryTPair) && (e0 & kEntryBlockMask) + g.nh * g.nw < g.nb) {
           // the same patch in frames t, t+1: one two-frame box per channel half
           int tt, hp, wp;
           block_coords(g, e0 & kEntryBlockMask, tt, hp, wp);
           const CUtensorMap* map = kind == 0 ? &a.map_k2 : &a.map_v2;
-          for (int c = c_lo; c < c_hi; ++c)
+          for (int c = 0; c < D / 64; ++c)
             tma_load_5d(&sm.slot[s][c][0], map, &sm.full[s], c * 64, wp * g.pw, hp * g.ph, tt * g.pt, bh);
         } else {
           const CUtensorMap* map = kind == 0 ? &a.map_k : &a.map_v;
@@ -368,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             int tt, hp, wp;
             block_coords(g, kb, tt, hp, wp);
-            for (int c = c_lo; c < c_hi; ++c)
+            for (int c = 0; c < D / 64; ++c)
               tma_load_5d(&sm.slot[s][c][e * 8192], map, &sm.full[s], c * 64, wp * g.pw, hp * g.ph,
                           tt * g.pt, bh);
           }
@@ -405,13 +336,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t kdesc0 = sw128_desc(smem_u32(&sm.slot[0][0][0]), 16, 1024);
       const uint64_t vdesc0 = sw128_desc(smem_u32(&sm.slot[0][0][0]), kChunkBytes, 1024);
       const uint64_t qdesc0 = sw128_desc(smem_u32(&sm.q[0][0][0]), 16, 1024);
-      const uint64_t qdesc1 = sw128_desc(smem_u32(&sm.q[split ? 0 : 1][0][0]), 16, 1024);
+      const uint64_t qdesc1 = sw128_desc(smem_u32(&sm.q[1][0][0]), 16, 1024);
       constexpr uint32_t kSlotStep = (D / 64) * kChunkBytes / 16;  // one slot, 16 B units
       const int u0 = __shfl_sync(0xFFFFFFFFu, tile[0].n_u, 0);
       const int u1 = __shfl_sync(0xFFFFFFFFu, tile[1].n_u, 0);
       const int n0 = (u0 + 1) >> 1, n1 = (u1 + 1) >> 1;
       bool ok = n0 == 0 || mbar_wait(&sm.q_full[0], 0, abort);  // (heaviest first: n1 <= n0)
-      if (!one_tile && ok && n1 > 0) ok = mbar_wait(&sm.q_full[1], 0, abort);
+      if (ok && n1 > 0) ok = mbar_wait(&sm.q_full[1], 0, abort);
       ok = __all_sync(0xFFFFFFFFu, ok);
       int k = 0;  // op index (ring position)
 #if SA_TRACE
@@ -424,15 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t kd = kdesc0 + uint64_t(s) * kSlotStep;
         const uint32_t id = ((x ? u1 : u0) - 2 * step) >= 2 ? id_s2 : id_s1;
         const uint32_t d_tmem = tmem + col_s(x);
-        if constexpr (kDiff) {
-          // map x: K steps of channels [x D/2, (x + 1) D/2) of the one Q tile
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
-            const int ks = x * (D / 32) + kk;
-            const uint32_t off = (uint32_t(ks >> 2) * kChunkBytes + uint32_t(ks & 3) * 32u) >> 4;
-            mma_ss(d_tmem, qdesc0 + off, kd + off, id, kk > 0);
-          }
-        } else if constexpr (D == 128) {
+        if constexpr (D == 128) {
           mma_ss_k8<kChunkBytes>(d_tmem, qd, kd, id, 0u);
         } else {
 #pragma unroll
@@ -539,8 +462,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    RelBiasRow rb;
-    if constexpr (kBias) rb = relbias_row(g, half && t.qb >= 0 ? t.qb : t.qa, r & 63, 1);
     for (int j = 0; j < t.nsteps; ++j) {
       const int nblk = step_blocks(t, j);
       const int e0 = list_at(t, 2 * j);
@@ -568,11 +489,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(s_col + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
       }
       tmem_wait_ld();
-      if constexpr (kBias) {
-        // log2 units, bias included, before the maximum is taken
-        if (keep0) relbias_add64<M == AttnMode::kBias8>(bias, rb, g, e0 & kEntryBlockMask, sl2, &sv[0]);
-        if (keep1) relbias_add64<M == AttnMode::kBias8>(bias, rb, g, e1 & kEntryBlockMask, sl2, &sv[64]);
-      }
       // row max over four independent chains (a single chain of 64 dependent
       // max3 would cost its full latency)
       float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -587,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mq[(i >> 1) & 3] = max3(mq[(i >> 1) & 3], __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
       }
       float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-      if constexpr (!kBias) mx *= sl2;
+      mx *= sl2;
       const bool need = mx > m + kRescaleThreshold;  // false while mx = -inf
       const float m_new = need ? mx : m;
       const float alpha = need ? ex2_approx(m - m_new) : 1.f;  // m = -inf -> 0
@@ -608,17 +524,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // p = 2^(s * log2(e)/sqrt(d) - m), two columns per packed op;
       // kPolyPairsPer8 of every 8 column pairs take the FMA-pipe exp2.
       const uint64_t sl2x2 = f2_pack(sl2, sl2);
-      // (bias: a row whose offsets are all masked so far has m = -inf; p = 2^-inf = 0)
-      const float negm = kBias && m == -INFINITY ? 0.f : -m;
-      const uint64_t negm2 = f2_pack(negm, negm);
+      const uint64_t negm2 = f2_pack(-m, -m);
       uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};  // four independent packed sums
 #pragma unroll
       for (int i = 0; i < 64; ++i) {
         const bool kp = (2 * i) < 64 ? keep0 : keep1;
         uint32_t packed = 0u;
         if (kp) {
-          const uint64_t s2 = f2_pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
-          const uint64_t x2 = kBias ? f2_add(s2, negm2) : f2_fma(s2, sl2x2, negm2);
+          const uint64_t x2 =
+              f2_fma(f2_pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sl2x2,
+                     negm2);
           float x0, x1;
           f2_unpack(x2, x0, x1);
           uint64_t e2;
@@ -648,72 +563,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         g_attn_trace[kTraceSoftmax + (warp - 4) * 2 * kTraceSteps + 2 * j + 1] = clock64();
 #endif
     }
-    // ---- epilogue: O / l -> natural token position
     if (!ok) {
       fail(a.status, &sm.abort, kDevErrTimeoutSoftmax);
     } else {
-      const float inv = l > 0.f ? 1.0f / l : 0.f;
-      bool done = t.nsteps == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&sm.o_final[x], 0, abort));
-      const int other = x ? tile[0].nsteps : tile[1].nsteps;
-      if (M != AttnMode::kPlain && one_tile) {
-        // the rows of A and B meet here: their statistics, then both O's in TMEM
-        join.m[x][r] = m;
-        join.l[x][r] = l;
-        mbar_arrive(&join.full);
-        done = done && __all_sync(0xFFFFFFFFu, mbar_wait(&join.full, 0, abort)) &&
-               (other == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&sm.o_final[x ^ 1], 0, abort)));
-      }
-      if (!done) {
-        fail(a.status, &sm.abort, kDevErrTimeoutSoftmax);
-      } else if (t.qa >= 0 && (half == 0 || t.qb >= 0)) {  // uniform across the warp
+      if (t.nsteps == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&sm.o_final[x], 0, abort))) {
         tc_fence_after_sync();
-        const size_t row = size_t(bh) * g.S + block_row_token(g, half ? t.qb : t.qa, r & 63);
-        // log-sum-exp of the row's kept scaled scores (natural log): m is
-        // in log2 units and l is the sum relative to 2^m
-        const bool two_sums = M != AttnMode::kPlain && split;
-        float w0 = inv, w1 = 0.f;  // what O_A and O_B count in the output
-        if (M != AttnMode::kPlain && one_tile) {
-          const float m0 = join.m[0][r], m1 = join.m[1][r], l0 = join.l[0][r], l1 = join.l[1][r];
-          if constexpr (kDiff) {
-            w0 = l0 > 0.f ? 1.0f / l0 : 0.f;
-            w1 = l1 > 0.f ? 1.0f / l1 : 0.f;
-          } else {
-            // one softmax over both halves: exact, the statistics are fp32
-            const float top = fmaxf(m0, m1);
-            const float e0 = l0 > 0.f ? ex2_approx(m0 - top) : 0.f;
-            const float e1 = l1 > 0.f ? ex2_approx(m1 - top) : 0.f;
-            l = l0 * e0 + l1 * e1;
-            m = top;
-            w0 = l > 0.f ? e0 / l : 0.f;
-            w1 = l > 0.f ? e1 / l : 0.f;
-          }
-        }
-        if (a.lse != nullptr && !(two_sums && x == 1))
-          a.lse[row + (kDiff ? size_t(x) * g.BH * g.S : 0)] =
-              l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
-        if (M != AttnMode::kPlain && one_tile) {
-          // A's warps write the first half of the channels, B's the second
-          const float lam = kDiff ? __bfloat162float(a.lam[bh % a.H]) : -1.f;
-          const int na = tile[0].nsteps, nb_ = tile[1].nsteps;
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const int col = x * (D / 2) + 32 * c;
-            float o1[32], o2[32];
-            load_o32(t_lane + col_o(0) + uint32_t(col), na, w0, o1);
-            load_o32(t_lane + col_o(1) + uint32_t(col), nb_, w1, o2);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o1[i] = fmaf(-lam, o2[i], o1[i]);
-            store_o32(a.out, row * D + col, o1, a.out_fp32);
-            if (kDiff && a.out2 != nullptr) store_o32(a.out2, row * D + col, o2, a.out_fp32);
-          }
-        } else {
+        // ---- epilogue: O / l -> natural token position
+        if (t.qa >= 0 && (half == 0 || t.qb >= 0)) {
+          const int blk = half ? t.qb : t.qa;
+          int tt, hp, wp;
+          block_coords(g, blk, tt, hp, wp);
+          // row i of the block: frame tt*pt + (i >> (lph + lpw)), row
+          // hp*ph + ((i >> lpw) & (ph - 1)), column wp*pw + (i & (pw - 1))
+          const int i = r & 63;
+          const int run = i >> g.lpw;
+          const size_t tok = (size_t(tt) * g.pt + (run >> g.lph)) * g.Hh * g.Ww +
+                             size_t(hp * g.ph + (run & (g.ph - 1))) * g.Ww +
+                             size_t(wp * g.pw + (i & (g.pw - 1)));
+          const size_t row = size_t(bh) * g.S + tok;
+          const float inv = l > 0.f ? 1.0f / l : 0.f;
+          // log-sum-exp of the row's kept scaled scores (natural log): m is
+          // in log2 units and l is the sum relative to 2^m
+          if (a.lse != nullptr)
+            a.lse[row] = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            load_o32(o_col + 32 * c, t.nsteps, inv, o);
-            store_o32(a.out, row * D + 32 * c, o, a.out_fp32);
+            uint32_t o[32];
+            if (t.nsteps > 0) {
+              tmem_ld32(o_col + 32 * c, o);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = 0u;
+            }
+            if (a.out_fp32) {
+              float4* dst =
+                  reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + 32 * c);
+#pragma unroll
+              for (int v4 = 0; v4 < 8; ++v4)
+                dst[v4] = make_float4(__uint_as_float(o[4 * v4]) * inv,
+                                      __uint_as_float(o[4 * v4 + 1]) * inv,
+                                      __uint_as_float(o[4 * v4 + 2]) * inv,
+                                      __uint_as_float(o[4 * v4 + 3]) * inv);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D +
+                                                    32 * c);
+#pragma unroll
+              for (int v8 = 0; v8 < 4; ++v8)
+                dst[v8] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * v8]) * inv,
+                                                 __uint_as_float(o[8 * v8 + 1]) * inv),
+                                     pack_bf16x2(__uint_as_float(o[8 * v8 + 2]) * inv,
+                                                 __uint_as_float(o[8 * v8 + 3]) * inv),
+                                     pack_bf16x2(__uint_as_float(o[8 * v8 + 4]) * inv,
+                                                 __uint_as_float(o[8 * v8 + 5]) * inv),
+                                     pack_bf16x2(__uint_as_float(o[8 * v8 + 6]) * inv,
+                                                 __uint_as_float(o[8 * v8 + 7]) * inv));
+            }
           }
         }
+      } else {
+        fail(a.status, &sm.abort, kDevErrTimeoutSoftmax);
       }
     }
   }
@@ -724,37 +633,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Up to four query tiles per SM, A and B take the halves of one tile's list: twice
-// the CTAs with half the steps each, where pairs of whole tiles leave SMs idle
-// (64 tiles: 37.6 -> 22.6 us; 576: 151 -> 149; 768: 262 -> 266; 3,552: 1,816 ->
-// 1,894, the join and the second prologue of each tile then being pure cost).
-constexpr long kSplitTiles = 4 * 148;
-
-template <int D, AttnMode M>
-static cudaError_t launch_attn_m(const AttnArgs& a, const Geometry& g, cudaStream_t stream) {
-  // At least 120 KB so that one CTA occupies an SM: each CTA allocates all
-  // 512 TMEM columns.
-  size_t need = sizeof(AttnSmem<D>) + 1024;
-  if (M != AttnMode::kPlain) need += sizeof(JoinSmem);
-  if (M == AttnMode::kBias || M == AttnMode::kBias8) need += relbias_offsets(g) * sizeof(float);
-  const size_t smem = need > 120 * 1024 ? need : 120 * 1024;
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, M>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e != cudaSuccess) return e;
-  const bool one_tile = M == AttnMode::kDiff || (M != AttnMode::kPlain && a.split);
-  const dim3 grid(unsigned(one_tile ? g.ntile : (g.ntile + 1) / 2), unsigned(g.BH));
-  attn_kernel<D, M><<<grid, kThreads, smem, stream>>>(a, g);
-  return cudaGetLastError();
-}
-
 template <int D>
 static cudaError_t launch_attn_d(const AttnArgs& a, const Geometry& g, cudaStream_t stream) {
-  if (a.lam != nullptr) return launch_attn_m<D, AttnMode::kDiff>(a, g, stream);
-  if (a.bias.table == nullptr) return launch_attn_m<D, AttnMode::kPlain>(a, g, stream);
-  AttnArgs b = a;
-  b.split = long(g.ntile) * g.BH <= kSplitTiles;
-  return g.lpw == 3 ? launch_attn_m<D, AttnMode::kBias8>(b, g, stream)
-                    : launch_attn_m<D, AttnMode::kBias>(b, g, stream);
+  // At least 120 KB so that one CTA occupies an SM: each CTA allocates all
+  // 512 TMEM columns.
+  const size_t need = sizeof(AttnSmem<D>) + 1024;
+  const size_t smem = need > 120 * 1024 ? need : 120 * 1024;
+  cudaError_t e = cudaFuncSetAttribute(attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(smem));
+  if (e != cudaSuccess) return e;
+  const dim3 grid(unsigned((g.ntile + 1) / 2), unsigned(g.BH));
+  attn_kernel<D><<<grid, kThreads, smem, stream>>>(a, g);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_attn(const AttnArgs& a, const Geometry& g, cudaStream_t stream) {

@@ -73,25 +73,6 @@ cudaError_t launch_mask_bytes(const MaskArgs& a, const uint8_t* mask, size_t hea
 cudaError_t launch_tile_order(const int32_t* tcnt, int32_t* order, const Geometry& g,
                               cudaStream_t stream);
 
-// Score functions of the attention kernel: q.k alone, with a relative position
-// bias (kBias8: blocks whose rows are 8 tokens, pw == 8, the patch among them;
-// kBias: any block shape), or the two maps of differential attention.
-enum class AttnMode { kPlain, kBias, kBias8, kDiff };
-
-// Learned relative position bias: row bh % H of table [H][n_buckets] (bf16), read
-// through bucket[], the table index of every offset along t, then h, then w
-// ((2T-1) + (2Hh-1) + (2Ww-1) entries, offset key - query, lowest first).
-// Offsets along the three axes, and the most that the kernels' shared memory
-// holds (T + Hh + Ww <= 512).
-SA_HD int relbias_offsets(const Geometry& g) { return 2 * (g.T + g.Hh + g.Ww) - 3; }
-constexpr int kRelBiasMaxAxes = 512;
-struct BiasArgs {
-  const __nv_bfloat16* table;  // null: no bias
-  const int32_t* bucket;
-  int n_buckets;
-  int H;
-};
-
 struct AttnArgs {
   CUtensorMap map_q, map_k, map_v;  // 5-D patch maps, see tma_host.h
   CUtensorMap map_k2, map_v2;       // the same with two-frame boxes
@@ -104,12 +85,6 @@ struct AttnArgs {
   int out_fp32;
   int debug_flags;
   float* lse;  // [BH][S] natural order: each row's log-sum-exp (natural log), or null
-               // (differential: [2][BH][S], one per map)
-  BiasArgs bias;             // relative position bias, or a null table
-  bool split;                // bias: one query tile per CTA, its list in two halves (set by the launch)
-  const __nv_bfloat16* lam;  // differential: [H] weights of the second map, or null
-  void* out2;                // differential: P_2 V [BH][S][d] like out, or null
-  int H;                     // differential: heads (bh % H picks lam's entry)
 };
 cudaError_t launch_attn(const AttnArgs& a, const Geometry& g, cudaStream_t stream);
 
@@ -175,6 +150,46 @@ cudaError_t launch_bwd(const BwdArgs& a, const Geometry& g, cudaStream_t stream)
 // dq = dq_acc (bf16 or fp32).
 cudaError_t launch_dq_convert(const float* dq_acc, void* dq, int out_fp32, const Geometry& g,
                               cudaStream_t stream);
+
+// Score functions besides q.k alone: a relative position bias (kBias8: blocks
+// whose rows are 8 tokens, pw == 8, the patch among them; kBias: any block
+// shape), or the two maps of differential attention.
+enum class AttnMode { kBias, kBias8, kDiff };
+
+// Learned relative position bias: row bh % H of table [H][n_buckets] (bf16), read
+// through bucket[], the table index of every offset along t, then h, then w
+// ((2T-1) + (2Hh-1) + (2Ww-1) entries, offset key - query, lowest first).
+// Offsets along the three axes, and the most that the kernels' shared memory
+// holds (T + Hh + Ww <= 512).
+SA_HD int relbias_offsets(const Geometry& g) { return 2 * (g.T + g.Hh + g.Ww) - 3; }
+constexpr int kRelBiasMaxAxes = 512;
+struct BiasArgs {
+  const __nv_bfloat16* table;  // null: no bias
+  const int32_t* bucket;
+  int n_buckets;
+  int H;
+};
+
+// Forward with a relative position bias (lam null) or of differential attention
+// (lam given) over the planned lists.
+struct ScoreFwdArgs {
+  CUtensorMap map_q, map_k, map_v;  // 5-D patch maps, one block per box
+  void* out;
+  void* out2;  // differential: P_2 V [BH][S][d] like out, or null
+  float* lse;  // [BH][S] (differential: [2][BH][S]) natural order, natural log, or null
+  const int32_t* tcnt;
+  const int32_t* tidx;
+  const int32_t* order;
+  BiasArgs bias;
+  const __nv_bfloat16* lam;  // [H] weights of the second map
+  int H;                     // heads (bh % H picks lam's entry)
+  uint32_t* status;
+  float scale_log2;  // log2(e) / sqrt(channels of a map)
+  int out_fp32;
+  int debug_flags;  // SA_DEBUG_STALL_LOADER: the first K load is never issued (test hook)
+  bool split;       // bias: one query tile per CTA, its list in halves (set by the launch)
+};
+cudaError_t launch_score_fwd(ScoreFwdArgs a, const Geometry& g, cudaStream_t stream);
 
 // Gradients with a relative position bias (lam null) or of differential
 // attention (lam given). Scratch regions as in ScoreBwdLayout.
