@@ -13,8 +13,8 @@
 // kernel (the SFU's 16 exponentials per cycle and SM alone are 1,024 cycles for a
 // step of both chains, the products 930 (differential) or 1,330 (bias)). One
 // stage of 128 keys per chain, as the plain kernel has it, took 2.04 ms where
-// this takes FWDDIFF (differential, 4 heads of 61,440 tokens) and 1.82 ms where
-// this takes FWDBIAS (bias, 12 x 37,632).
+// this takes 1.65 (differential, 4 heads of 61,440 tokens) and 1.82 ms where this
+// takes 1.50 (bias, 12 x 37,632).
 //
 //   warps 0, 2, 3  TMA producers, one 16 KB ring slot per block of K or V, in the
 //                  order the MMA warp consumes them; the maps share their slots
@@ -304,27 +304,30 @@ __global__ void __launch_bounds__(kFThreads, 1)
             if (!ok) break;
           }
           tc_fence_after_sync();
-          ready = false;
+          const int k_next = k + (!kDiff || x == 1 ? (has_s ? 2 : 1) : 0);
           if (one) {
             mma_ts_k<4>(col_o(x), col_s(x, j & 1), v0 + uint64_t(sv) * kSlotStep, id_pv,
                         j > 0 ? 1u : 0u);
             mma_commit(j + 1 < n ? &sm.pv_done[x] : &sm.o_final[x]);
             if (!kDiff || x == 1) mma_commit(&sm.empty[sv]);
+            // The next unit (the other chain's step, or the next one's): its barriers
+            // are looked at between this unit's products, since a shared-memory access
+            // waits for the MMAs issued before it (at a unit's end it left the tensor
+            // core idle for 250 of 770 cycles).
+            const int xn = x == 0 && j < nb_ ? 1 : (j + 1 < na ? 0 : 1);
+            const int jn = xn == 1 && x == 0 ? j : j + 1;
+            const int nn = xn ? nb_ : na;
+            ready = false;
+            if (jn < nn) {
+              const int s1 = k_next % kFSlots, s2 = (k_next + 1) % kFSlots;
+              const uint32_t par1 = (k_next / kFSlots) & 1, par2 = ((k_next + 1) / kFSlots) & 1;
+              ready = mbar_peek3(&sm.p_full[xn][jn & 1], (jn >> 1) & 1, &sm.full[s1], par1,
+                                 jn + 2 < nn ? &sm.full[s2] : &sm.full[s1],
+                                 jn + 2 < nn ? par2 : par1) == 7u;
+            }
             if (has_s) mma_s(x, j + 2, sk);
           }
-          if (!kDiff || x == 1) k += has_s ? 2 : 1;
-          // the next unit: the other chain's step, or the next one's
-          const int xn = x == 0 && j < nb_ ? 1 : (j + 1 < na ? 0 : 1);
-          const int jn = xn == 1 && x == 0 ? j : j + 1;
-          const int nn = xn ? nb_ : na;
-          if (one && jn < nn) {
-            const int s1 = k % kFSlots, s2 = (k + 1) % kFSlots;
-            const uint32_t r = mbar_peek3(
-                &sm.p_full[xn][jn & 1], (jn >> 1) & 1, &sm.full[s1], (k / kFSlots) & 1,
-                jn + 2 < nn ? &sm.full[s2] : &sm.full[s1],
-                jn + 2 < nn ? ((k + 1) / kFSlots) & 1 : (k / kFSlots) & 1);
-            ready = r == 7u;
-          }
+          k = k_next;
           __syncwarp();
         }
       }
