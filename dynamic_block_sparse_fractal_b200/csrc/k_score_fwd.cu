@@ -112,10 +112,16 @@ __device__ __forceinline__ void store_o32(void* out, size_t at, const float (&x)
 
 }  // namespace
 
-template <int D, AttnMode M>
+// L: log2 of the tokens in a row of a block where the bias is taken row by row
+// and column by column (24 values for the 64 keys at L = 3, held in registers);
+// kAnyShape: three lookups per key (284 us against 122 for 12 x 5,760 tokens in
+// blocks that both can take).
+constexpr int kAnyShape = -1;
+
+template <int D, AttnMode M, int L>
 __global__ void __launch_bounds__(kFThreads, 1)
     score_fwd_kernel(const __grid_constant__ ScoreFwdArgs a, const Geometry g) {
-  constexpr bool kDiff = M == AttnMode::kDiff, kRow8 = M == AttnMode::kBias8;
+  constexpr bool kDiff = M == AttnMode::kDiff, kRows = !kDiff && L != kAnyShape;
   const bool split = !kDiff && a.split;
   const bool one_tile = kDiff || split;
   extern __shared__ uint8_t sf_raw[];
@@ -358,10 +364,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
       const int ent = t.at(j);
       const bool keep = (ent & keep_bit) != 0;  // uniform across the warp
       // the bias of the step's keys, while their scores are computed
-      float f8[8];
-      uint64_t g8[4];
-      if constexpr (kRow8) {
-        if (keep) relbias_rows8(bias, rb, g, ent & kEntryBlockMask, f8, g8);
+      BlockBias<kRows ? L : 3> bb;
+      if constexpr (kRows) {
+        if (keep) bb.load(bias, rb, g, ent & kEntryBlockMask);
       }
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.s_full[x][j & 1], (j >> 1) & 1, abort));
       if (!ok) break;
@@ -373,8 +378,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
         tmem_ld32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
         tmem_ld32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
         tmem_wait_ld();
-        if constexpr (kRow8) {
-          mx = relbias_cols8(f8, g8, sl2, sv);  // log2 units, sv without the rows' f
+        if constexpr (kRows) {
+          mx = bb.add_cols(sl2, sv);  // log2 units, sv without the rows' f
         } else {
           if constexpr (!kDiff) relbias_add64(bias, rb, g, ent & kEntryBlockMask, sl2, sv);
           float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -415,8 +420,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
         for (int i = 0; i < 32; ++i) {
           const uint64_t s2 = f2_pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
           uint64_t x2;
-          if constexpr (kRow8) {
-            const float fm = f8[i >> 2] + negm;
+          if constexpr (kRows) {
+            const float fm = bb.f[2 * i >> L] + negm;
             x2 = f2_add(s2, f2_pack(fm, fm));
           } else {
             x2 = kDiff ? f2_fma(s2, sl2x2, negm2) : f2_add(s2, negm2);
@@ -513,28 +518,32 @@ __global__ void __launch_bounds__(kFThreads, 1)
 // the CTAs with half the steps each, where pairs of whole tiles leave SMs idle.
 constexpr long kSplitTiles = 4 * 148;
 
-template <int D, AttnMode M>
+template <int D, AttnMode M, int L>
 static cudaError_t launch_score_fwd_m(const ScoreFwdArgs& a, const Geometry& g,
                                       cudaStream_t stream) {
   // At least 120 KB: each CTA allocates all 512 TMEM columns.
   size_t need = sizeof(ScoreFwdSmem<D>) + 1024;
   if (M != AttnMode::kDiff) need += relbias_offsets(g) * sizeof(float);
   const int smem = int(need > 120 * 1024 ? need : 120 * 1024);
-  cudaError_t e = cudaFuncSetAttribute(score_fwd_kernel<D, M>,
+  cudaError_t e = cudaFuncSetAttribute(score_fwd_kernel<D, M, L>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const bool one_tile = M == AttnMode::kDiff || a.split;
   const dim3 grid(unsigned(one_tile ? g.ntile : (g.ntile + 1) / 2), unsigned(g.BH));
-  score_fwd_kernel<D, M><<<grid, kFThreads, smem, stream>>>(a, g);
+  score_fwd_kernel<D, M, L><<<grid, kFThreads, smem, stream>>>(a, g);
   return cudaGetLastError();
 }
 
 template <int D>
 static cudaError_t launch_score_fwd_d(const ScoreFwdArgs& a, const Geometry& g,
                                       cudaStream_t stream) {
-  if (a.lam != nullptr) return launch_score_fwd_m<D, AttnMode::kDiff>(a, g, stream);
-  return g.lpw == 3 ? launch_score_fwd_m<D, AttnMode::kBias8>(a, g, stream)
-                    : launch_score_fwd_m<D, AttnMode::kBias>(a, g, stream);
+  if (a.lam != nullptr) return launch_score_fwd_m<D, AttnMode::kDiff, kAnyShape>(a, g, stream);
+  switch (g.lpw) {
+    case 2: return launch_score_fwd_m<D, AttnMode::kBias, 2>(a, g, stream);
+    case 3: return launch_score_fwd_m<D, AttnMode::kBias, 3>(a, g, stream);
+    case 4: return launch_score_fwd_m<D, AttnMode::kBias, 4>(a, g, stream);
+    default: return launch_score_fwd_m<D, AttnMode::kBias, kAnyShape>(a, g, stream);
+  }
 }
 
 cudaError_t launch_score_fwd(ScoreFwdArgs a, const Geometry& g, cudaStream_t stream) {

@@ -151,10 +151,9 @@ cudaError_t launch_bwd(const BwdArgs& a, const Geometry& g, cudaStream_t stream)
 cudaError_t launch_dq_convert(const float* dq_acc, void* dq, int out_fp32, const Geometry& g,
                               cudaStream_t stream);
 
-// Score functions besides q.k alone: a relative position bias (kBias8: blocks
-// whose rows are 8 tokens, pw == 8, the patch among them; kBias: any block
-// shape), or the two maps of differential attention.
-enum class AttnMode { kBias, kBias8, kDiff };
+// Score functions besides q.k alone: a relative position bias, or the two maps of
+// differential attention.
+enum class AttnMode { kBias, kDiff };
 
 // Learned relative position bias: row bh % H of table [H][n_buckets] (bf16), read
 // through bucket[], the table index of every offset along t, then h, then w

@@ -73,43 +73,48 @@ __device__ __forceinline__ void relbias_block(const Geometry& g, const RelBiasRo
   w = r.w + sign * ((rest - hb * g.nw) * g.pw);
 }
 
-// The bias of 64 keys of block kb when the block's rows are 8 tokens (pw == 8):
-// f[a] of each row of the block, g of its columns in pairs.
-__device__ __forceinline__ void relbias_rows8(const float* bias, const RelBiasRow& r,
-                                              const Geometry& geo, int kb, float (&f)[8],
-                                              uint64_t (&g)[4]) {
-  int t, h, w;
-  relbias_block(geo, r, kb, 1, t, h, w);
-#pragma unroll
-  for (int a = 0; a < 8; ++a) f[a] = bias[t + (a >> geo.lph)] + bias[h + (a & (geo.ph - 1))];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) g[c] = f2_pack(bias[w + 2 * c], bias[w + 2 * c + 1]);
-}
+// The bias of 64 keys of block kb whose rows are 2^L tokens (pw == 2^L): f[a] of
+// each row of the block, g of its columns in pairs.
+template <int L>
+struct BlockBias {
+  static constexpr int kRows = 64 >> L, kPairs = (1 << L) / 2;
+  float f[kRows];
+  uint64_t g[kPairs];
 
-// x[i] = x[i] * sl2 + g for those 64 keys (raw scores in, log2 units less f out);
-// returns the largest x + f.
-__device__ __forceinline__ float relbias_cols8(const float (&f)[8], const uint64_t (&g)[4],
-                                               float sl2, uint32_t* x) {
-  const uint64_t sl2x2 = f2_pack(sl2, sl2);
-  float top = -INFINITY;
+  __device__ __forceinline__ void load(const float* bias, const RelBiasRow& r, const Geometry& geo,
+                                       int kb) {
+    int t, h, w;
+    relbias_block(geo, r, kb, 1, t, h, w);
 #pragma unroll
-  for (int a = 0; a < 8; ++a) {
-    float m[4];
+    for (int a = 0; a < kRows; ++a) f[a] = bias[t + (a >> geo.lph)] + bias[h + (a & (geo.ph - 1))];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int i = 8 * a + 2 * c;
-      const uint64_t y =
-          f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sl2x2, g[c]);
-      float y0, y1;
-      f2_unpack(y, y0, y1);
-      x[i] = __float_as_uint(y0);
-      x[i + 1] = __float_as_uint(y1);
-      m[c] = fmaxf(y0, y1);
-    }
-    top = fmaxf(top, max3(fmaxf(m[0], m[1]), m[2], m[3]) + f[a]);
+    for (int c = 0; c < kPairs; ++c) g[c] = f2_pack(bias[w + 2 * c], bias[w + 2 * c + 1]);
   }
-  return top;
-}
+
+  // x[i] = x[i] * sl2 + g for those 64 keys (raw scores in, log2 units less f out);
+  // returns the largest x + f.
+  __device__ __forceinline__ float add_cols(float sl2, uint32_t* x) const {
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+    float top = -INFINITY;
+#pragma unroll
+    for (int a = 0; a < kRows; ++a) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < kPairs; ++c) {
+        const int i = (a << L) + 2 * c;
+        const uint64_t y =
+            f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sl2x2, g[c]);
+        float y0, y1;
+        f2_unpack(y, y0, y1);
+        x[i] = __float_as_uint(y0);
+        x[i + 1] = __float_as_uint(y1);
+        m = max3(m, y0, y1);
+      }
+      top = fmaxf(top, m + f[a]);
+    }
+    return top;
+  }
+};
 
 // x[i] = x[i] * sl2 + bias for the 64 keys of block kb, any block shape.
 __device__ __forceinline__ void relbias_add64(const float* bias, const RelBiasRow& r,
