@@ -392,6 +392,7 @@ def plan_mask(desc: SaDesc, mask: torch.Tensor, workspace: torch.Tensor, stream=
             not mask.is_contiguous() or tuple(mask.shape) not in shapes:
         raise ValueError("mask must be a contiguous bool or uint8 CUDA tensor shaped [nb, nb], "
                          "[B*H, nb, nb] or [B, H, nb, nb]")
+    _same_device(workspace, mask)
     heads = 1 if mask.dim() == 2 else desc.B * desc.H
     _ok(lib().sparse_attn_plan_mask(ctypes.byref(desc), _ptr(mask), heads, _ptr(workspace),
                                     workspace.numel(), _stream(stream)), "plan_mask")
@@ -437,13 +438,23 @@ def _check_like(name: str, t: torch.Tensor, dtype, shape) -> torch.Tensor:
 
 
 def _same_device(q: torch.Tensor, *ts: Optional[torch.Tensor]) -> None:
-    """Every tensor on q's device, and that device current (its streams are)."""
+    """Every tensor on the first one's device, and that device current (its streams are)."""
     dev = q.get_device()
     for t in ts:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"all tensors must be on q's device ({q.device}), got {t.device}")
+            raise ValueError(f"all tensors must be on one device, got {q.device} and {t.device}")
     if dev != torch.cuda.current_device():
-        raise ValueError(f"q is on {q.device}, which is not the current device")
+        raise ValueError(f"the tensors are on {q.device}, which is not the current device")
+
+
+def _new_like(q: torch.Tensor, dtype, stream) -> torch.Tensor:
+    if stream is None and dtype == q.dtype:
+        return torch.empty_like(q)
+    return _new(q.shape, dtype, q.device, stream)
+
+
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _new(shape, dtype, device, stream) -> torch.Tensor:
@@ -466,20 +477,20 @@ def fwd_bias(desc: SaDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ta
     want = torch.float32 if desc.out_fp32 else torch.bfloat16
     rel = _rel_bias(desc, table, bucket)
     if out is None:
-        out = _new(q.shape, want, q.device, stream)
+        out = _new_like(q, want, stream)
     else:
         _check_like("out", out, want, q.shape)
     if lse is not None:
         _check_like("lse", lse, torch.float32, q.shape[:3])
     _same_device(q, k, v, table, bucket, workspace, out, lse)
-    _ok(lib().sparse_attn_fwd_bias(ctypes.byref(desc), ctypes.byref(rel), _ptr(q), _ptr(k), _ptr(v),
-                                   _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse),
+    _ok(lib().sparse_attn_fwd_bias(ctypes.byref(desc), ctypes.byref(rel), _at(q), _at(k), _at(v),
+                                   _at(workspace), workspace.numel(), _at(out), _at(lse),
                                    _stream(stream)), "fwd_bias")
     return out
 
 
 def _grads(q: torch.Tensor, want, given, stream):
-    return [_new(q.shape, want, q.device, stream) if g is None else
+    return [_new_like(q, want, stream) if g is None else
             _check_like(n, g, want, q.shape) for n, g in zip(("dq", "dk", "dv"), given)]
 
 
@@ -501,13 +512,13 @@ def bwd_bias(desc: SaDesc, q, k, v, table, bucket, out, dout, lse, workspace, dq
     _check_like("out", out, want, q.shape)
     _check_like("lse", lse, torch.float32, q.shape[:3])
     grads = _grads(q, want, (dq, dk, dv), stream)
-    grads.append(_new(table.shape, want, q.device, stream) if dtable is None else
+    grads.append(_new_like(table, want, stream) if dtable is None else
                  _check_like("dtable", dtable, want, table.shape))
     scratch = _score_scratch(desc, lib().sparse_attn_bwd_bias_scratch_size, scratch, q.device, stream)
     _same_device(q, k, v, table, bucket, workspace, out, dout, lse, scratch, *grads)
-    _ok(lib().sparse_attn_bwd_bias(ctypes.byref(desc), ctypes.byref(rel), _ptr(q), _ptr(k), _ptr(v),
-                                   _ptr(out), _ptr(dout), _ptr(lse), _ptr(workspace),
-                                   workspace.numel(), *[_ptr(g) for g in grads], _ptr(scratch),
+    _ok(lib().sparse_attn_bwd_bias(ctypes.byref(desc), ctypes.byref(rel), _at(q), _at(k), _at(v),
+                                   _at(out), _at(dout), _at(lse), _at(workspace),
+                                   workspace.numel(), *[_at(g) for g in grads], _at(scratch),
                                    scratch.numel(), _stream(stream)), "bwd_bias")
     return tuple(grads)
 
@@ -527,7 +538,7 @@ def fwd_diff(desc: SaDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, la
     want = torch.float32 if desc.out_fp32 else torch.bfloat16
     _check_lam(desc, lam)
     if out is None:
-        out = _new(q.shape, want, q.device, stream)
+        out = _new_like(q, want, stream)
     else:
         _check_like("out", out, want, q.shape)
     if out2 is not None:
@@ -535,9 +546,9 @@ def fwd_diff(desc: SaDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, la
     if lse is not None:
         _check_like("lse", lse, torch.float32, (2,) + tuple(q.shape[:3]))
     _same_device(q, k, v, lam, workspace, out, out2, lse)
-    _ok(lib().sparse_attn_fwd_diff(ctypes.byref(desc), _ptr(lam), _ptr(q), _ptr(k), _ptr(v),
-                                   _ptr(workspace), workspace.numel(), _ptr(out), _ptr(out2),
-                                   _ptr(lse), _stream(stream)), "fwd_diff")
+    _ok(lib().sparse_attn_fwd_diff(ctypes.byref(desc), _at(lam), _at(q), _at(k), _at(v),
+                                   _at(workspace), workspace.numel(), _at(out), _at(out2),
+                                   _at(lse), _stream(stream)), "fwd_diff")
     return out
 
 
@@ -552,13 +563,13 @@ def bwd_diff(desc: SaDesc, q, k, v, lam, out, out2, dout, lse, workspace, dq=Non
     _check_like("out2", out2, want, q.shape)
     _check_like("lse", lse, torch.float32, (2,) + tuple(q.shape[:3]))
     grads = _grads(q, want, (dq, dk, dv), stream)
-    grads.append(_new(lam.shape, want, q.device, stream) if dlam is None else
+    grads.append(_new_like(lam, want, stream) if dlam is None else
                  _check_like("dlam", dlam, want, lam.shape))
     scratch = _score_scratch(desc, lib().sparse_attn_bwd_diff_scratch_size, scratch, q.device, stream)
     _same_device(q, k, v, lam, workspace, out, out2, dout, lse, scratch, *grads)
-    _ok(lib().sparse_attn_bwd_diff(ctypes.byref(desc), _ptr(lam), _ptr(q), _ptr(k), _ptr(v),
-                                   _ptr(out), _ptr(out2), _ptr(dout), _ptr(lse), _ptr(workspace),
-                                   workspace.numel(), *[_ptr(g) for g in grads], _ptr(scratch),
+    _ok(lib().sparse_attn_bwd_diff(ctypes.byref(desc), _at(lam), _at(q), _at(k), _at(v),
+                                   _at(out), _at(out2), _at(dout), _at(lse), _at(workspace),
+                                   workspace.numel(), *[_at(g) for g in grads], _at(scratch),
                                    scratch.numel(), _stream(stream)), "bwd_diff")
     return tuple(grads)
 

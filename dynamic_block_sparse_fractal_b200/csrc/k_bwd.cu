@@ -15,6 +15,7 @@
 
 #include "kernels.cuh"
 #include "sm100.cuh"
+#include "transposed.cuh"
 
 namespace sa {
 
@@ -82,36 +83,11 @@ cudaError_t launch_bwd_prep(const void* o, const void* do_, const float* lse, fl
   return cudaGetLastError();
 }
 
-// One warp per (bh, key tile): scan every q-block's keep bitmap for the
-// tile's two k-blocks (the query-tile pairing applied to keys) and compact
-// the q-blocks keeping either, ascending.
+// Transposed lists, one warp per (bh, key tile).
 __global__ void __launch_bounds__(256)
     bwd_lists_kernel(const uint32_t* __restrict__ bits, int32_t* __restrict__ kcnt,
                      int32_t* __restrict__ kidx, Geometry g) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long unit = long(blockIdx.x) * 8 + warp;
-  if (unit >= long(g.BH) * g.ntile) return;
-  const int bh = int(unit / g.ntile), tile = int(unit - long(bh) * g.ntile);
-  int ka, kb;
-  tile_blocks(g, tile, ka, kb);
-  const int words = bitmap_words(g);
-  const uint32_t* rows = bits + size_t(bh) * g.nb * words;
-  int32_t* out = kidx + size_t(unit) * g.nb;
-  int n = 0;
-  for (int i0 = 0; i0 < g.nb; i0 += 32) {
-    const int i = i0 + lane;
-    bool a = false, b = false;
-    if (i < g.nb) {
-      a = (rows[size_t(i) * words + (ka >> 5)] >> (ka & 31)) & 1u;
-      if (kb >= 0) b = (rows[size_t(i) * words + (kb >> 5)] >> (kb & 31)) & 1u;
-    }
-    const unsigned m = __ballot_sync(0xFFFFFFFFu, a || b);
-    if (a || b)
-      out[n + __popc(m & ((1u << lane) - 1u))] =
-          i | (a ? kEntryKeepA : 0) | (b ? kEntryKeepB : 0);
-    n += __popc(m);
-  }
-  if (lane == 0) kcnt[unit] = n;
+  transposed_list(bits, kcnt, kidx, g, long(blockIdx.x) * 8 + (threadIdx.x >> 5));
 }
 
 cudaError_t launch_bwd_lists(const uint32_t* bits, int32_t* kcnt, int32_t* kidx, const Geometry& g,

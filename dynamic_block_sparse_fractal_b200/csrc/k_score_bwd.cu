@@ -34,6 +34,7 @@
 #include "kernels.cuh"
 #include "exp2_poly.cuh"
 #include "relbias.cuh"
+#include "transposed.cuh"
 #include "sm100.cuh"
 
 namespace sa {
@@ -368,7 +369,8 @@ static_assert(sizeof(SbSmem<128, 4>) + 1024 + sizeof(float) * (2 * kRelBiasMaxAx
 
 // -D_m and -lse_m * log2(e) of every row into fractal order (negated: both are
 // addends; an empty row's lse = -inf stays -inf, so that 2^(z - lse) is 0). D/8 lanes per row, 32 rows
-// per CTA, one head per CTA.
+// per CTA, one head per CTA. The CTAs behind those make the transposed lists (see
+// transposed_list), which need nothing from them: one launch less.
 constexpr int kPrepRows = 32;
 
 template <int D, bool kDiff>
@@ -376,13 +378,20 @@ __global__ void __launch_bounds__(256)
     score_prep_kernel(const void* __restrict__ o, const void* __restrict__ o2,
                       const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse,
                       const __nv_bfloat16* __restrict__ lam, int H, float* __restrict__ nlse,
-                      float* __restrict__ ndsum, int fp32, Geometry g) {
+                      float* __restrict__ ndsum, int fp32, int row_ctas,
+                      const uint32_t* __restrict__ bits, int32_t* __restrict__ kcnt,
+                      int32_t* __restrict__ kidx, Geometry g) {
+  const int per_head = (g.S + kPrepRows - 1) / kPrepRows;
+  if (int(blockIdx.x) >= row_ctas) {
+    transposed_list(bits, kcnt, kidx, g, long(int(blockIdx.x) - row_ctas) * 8 + (threadIdx.x >> 5));
+    return;
+  }
   constexpr int kLanes = D / 8;
-  const int sub = threadIdx.x % kLanes, bh = blockIdx.y;
+  const int sub = threadIdx.x % kLanes, bh = int(blockIdx.x) / per_head;
   const size_t all = size_t(g.BH) * g.S;
   const float lm = kDiff ? __bfloat162float(lam[bh % H]) : 0.f;
   for (int i = threadIdx.x / kLanes; i < kPrepRows; i += 256 / kLanes) {
-    const int pos = blockIdx.x * kPrepRows + i;
+    const int pos = (int(blockIdx.x) - bh * per_head) * kPrepRows + i;
     if (pos >= g.S) break;
     const size_t row = size_t(bh) * g.S + block_row_token(g, pos >> 6, pos & 63);
     const size_t at = row * D + 8 * sub;
@@ -1053,11 +1062,13 @@ static cudaError_t launch_score_bwd_d(const ScoreBwdArgs& a, const Geometry& g,
 
 cudaError_t launch_score_bwd(ScoreBwdArgs a, const Geometry& g, cudaStream_t stream) {
   a.group = head_group(g);
-  const dim3 grid(unsigned((g.S + kPrepRows - 1) / kPrepRows), unsigned(g.BH));
+  const int row_ctas = (g.S + kPrepRows - 1) / kPrepRows * g.BH;
+  const unsigned grid = unsigned(row_ctas) + unsigned((long(g.BH) * g.ntile + 7) / 8);
   const bool diff = a.lam != nullptr;
 #define SA_PREP(D, DIFF)                                                                       \
   score_prep_kernel<D, DIFF><<<grid, 256, 0, stream>>>(a.out, a.out2, a.dout, a.lse, a.lam, a.H, \
-                                                       a.nlse, a.ndsum, a.out_fp32, g)
+                                                       a.nlse, a.ndsum, a.out_fp32, row_ctas,   \
+                                                       a.bits, a.kcnt, a.kidx, g)
   if (g.d == 128) {
     if (diff) SA_PREP(128, true); else SA_PREP(128, false);
   } else {
@@ -1065,7 +1076,6 @@ cudaError_t launch_score_bwd(ScoreBwdArgs a, const Geometry& g, cudaStream_t str
   }
 #undef SA_PREP
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_bwd_lists(a.bits, a.kcnt, a.kidx, g, stream);
   // (no order where every key tile starts at once)
   if (long(g.ntile) * g.BH <= 148) a.korder = nullptr;
   else if (e == cudaSuccess) e = launch_tile_order(a.kcnt, a.korder, g, stream);

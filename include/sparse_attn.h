@@ -443,12 +443,17 @@ sa_status sparse_attn_plan_mask(const sa_desc* desc, const uint8_t* mask, int ma
  * Attention over the planned blocks with a learned bias on each score:
  *   z_ij = q_i . k_j / sqrt(d) + b_t[t_j - t_i] + b_h[h_j - h_i] + b_w[w_j - w_i]
  * where (t, h, w) are a token's frame, row and column and each b_* reads the
- * head's row of a table through a map from offsets to buckets. */
+ * head's row of a table through a map from offsets to buckets. As for
+ * sparse_attn_fwd, q, k and v have to be finite in every block that the row or
+ * the other q-block of its tile keeps (a dropped pair counts as 0 times its
+ * value). */
 typedef struct sa_rel_bias {
   const void* table;     /* device bf16 [H][n_buckets], 2-byte aligned, in nats:
                             row h serves head h of every batch entry. An entry at
                             or below -1e30 (the type's lowest value, -inf) masks
-                            its offsets; other entries must be finite */
+                            its offsets; other entries must be finite (P is
+                            rebuilt from z and its log-sum-exp in fp32: relative
+                            error about 2^-22 |z|) */
   const int32_t* bucket; /* device int32, 4-byte aligned: the table index of every
                             offset key - query, lowest first: the 2T-1 along t, then
                             the 2Hh-1 along h, then the 2Ww-1 along w. Axes may

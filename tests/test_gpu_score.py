@@ -236,6 +236,17 @@ def test_densities(density):
     p.check_ok()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_tiles_than_one_wave(d):
+    """600 query tiles, 5 a head: two tiles per CTA in the biased forward (a lone one in
+    each head's last), key tiles sorted, heads dealt out in groups."""
+    p = Problem((10, 12, 3, 8, 24, d, None, False), seed=13, density=0.4)
+    q, k, v, g = p.dev()
+    check_bias(p, *run_bias(p, q, k, v, g, p.table.cuda(), torch.from_numpy(p.bucket).cuda()))
+    check_diff(p, *run_diff(p, q, k, v, g, p.lam.cuda()))
+    p.check_ok()
+
+
 def test_masked_offsets():
     """Entries of -inf and of the lowest value mask; a row with all offsets masked is
     one that keeps nothing."""
