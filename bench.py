@@ -77,7 +77,7 @@ def kept_flops_per_pair(w):
 ATTN_TRAFFIC = {
     "workload": "hunyuan_1x24x126720x128",
     "bytes": 12 * (383.973888e6 + 61.027584e6),
-    "sources_sha1": "8ed27f31aeb2798a0dc67b008dd694bdb3f8774c",
+    "sources_sha1": "72d7e7ba65e1851e3e5e1ec31e63e0ed6d778a32",
 }
 ATTN_SOURCES = ("k_attn.cu", "sm100.cuh", "exp2_poly.cuh", "layout.cuh")
 

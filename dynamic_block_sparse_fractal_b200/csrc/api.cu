@@ -413,8 +413,8 @@ sa_status sparse_attn_plan_mask(const sa_desc* desc, const uint8_t* mask, int ma
   m.tidx = at<int32_t>(workspace, w.tidx);
   m.status = at<uint32_t>(workspace, w.status);
   const size_t head = mask_heads == 1 ? 0 : size_t(g.nb) * g.nb;
-  if (launch_mask_bytes(m, mask, head, g, s) != cudaSuccess) return SA_ERR_CUDA;
-  return cuda_status(launch_tile_order(m.tcnt, at<int32_t>(workspace, w.order), g, s));
+  return cuda_status(
+      launch_mask_bytes(m, mask, head, at<int32_t>(workspace, w.order), g, s));
 }
 
 // The forward with a bias, or of differential attention (lambda given).

@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int u0 = __shfl_sync(0xFFFFFFFFu, tile[0].n_u, 0);
       const int u1 = __shfl_sync(0xFFFFFFFFu, tile[1].n_u, 0);
       const int n0 = (u0 + 1) >> 1, n1 = (u1 + 1) >> 1;
-      bool ok = n0 == 0 || mbar_wait(&sm.q_full[0], 0, abort);  // (heaviest first: n1 <= n0)
+      bool ok = n0 == 0 || mbar_wait(&sm.q_full[0], 0, abort);
       if (ok && n1 > 0) ok = mbar_wait(&sm.q_full[1], 0, abort);
       ok = __all_sync(0xFFFFFFFFu, ok);
       int k = 0;  // op index (ring position)

@@ -65,9 +65,10 @@ bool radius_supported(const Geometry& g);
 
 // The caller's block mask (bytes, 0 = dropped; [BH][nb][nb], or one [nb][nb]
 // for all heads when head_stride is 0) as bitmaps, counts, ascending lists and
-// per-tile union lists (a's fields of these names); clears a.status.
+// per-tile union lists (a's fields of these names) and the tile order; clears
+// a.status.
 cudaError_t launch_mask_bytes(const MaskArgs& a, const uint8_t* mask, size_t head_stride,
-                              const Geometry& g, cudaStream_t stream);
+                              int32_t* order, const Geometry& g, cudaStream_t stream);
 
 // Per head: tiles sorted by descending union length (ties by tile index).
 cudaError_t launch_tile_order(const int32_t* tcnt, int32_t* order, const Geometry& g,
