@@ -466,8 +466,8 @@ __global__ void __launch_bounds__(kSbThreads, 1)
   using Smem = SbSmem<D, kSlots>;
   constexpr uint32_t kColX = 0, kColY = 128, kStage0 = 256, kStage = 128, kDP = W * NM;
   extern __shared__ uint8_t sb_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>(
-      (reinterpret_cast<uintptr_t>(sb_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not an address rounded up: the compiler then knows shared memory)
+  Smem& sm = *reinterpret_cast<Smem*>(sb_raw + ((0u - smem_u32(sb_raw)) & 1023u));
   SbBars& br = sm.bar;
   float* bias = reinterpret_cast<float*>(&sm + 1);
   const int noff = relbias_offsets(g);

@@ -13,8 +13,8 @@
 // kernel (the SFU's 16 exponentials per cycle and SM alone are 1,024 cycles for a
 // step of both chains, the products 930 (differential) or 1,330 (bias)). One
 // stage of 128 keys per chain, as the plain kernel has it, took 2.04 ms where
-// this takes 1.65 (differential, 4 heads of 61,440 tokens) and 1.82 ms where this
-// takes 1.50 (bias, 12 x 37,632).
+// this takes 1.68 (differential, 4 heads of 61,440 tokens) and 1.82 ms where this
+// takes 1.45 (bias, 12 x 37,632).
 //
 //   warps 0, 2, 3  TMA producers, one 16 KB ring slot per block of K or V, in the
 //                  order the MMA warp consumes them; the maps share their slots
@@ -125,8 +125,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
   const bool split = !kDiff && a.split;
   const bool one_tile = kDiff || split;
   extern __shared__ uint8_t sf_raw[];
-  ScoreFwdSmem<D>& sm = *reinterpret_cast<ScoreFwdSmem<D>*>(
-      (reinterpret_cast<uintptr_t>(sf_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not an address rounded up: the compiler then knows shared memory)
+  ScoreFwdSmem<D>& sm =
+      *reinterpret_cast<ScoreFwdSmem<D>*>(sf_raw + ((0u - smem_u32(sf_raw)) & 1023u));
   float* bias = reinterpret_cast<float*>(&sm + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y;
