@@ -767,48 +767,48 @@ __global__ void __launch_bounds__(kSbThreads, 1)
               }
             }
 #pragma unroll
-          for (int k = k4; k < k4 + 4; k += 2) {
-            const uint64_t e2 = f2_pack(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1]));
-            uint64_t p2[NM];
+            for (int k = k4; k < k4 + 4; k += 2) {
+              const uint64_t e2 = f2_pack(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1]));
+              uint64_t p2[NM];
 #pragma unroll
-            for (int m = 0; m < NM; ++m) {
-              uint64_t nl2, nd2;
-              if (kQ) {
-                nl2 = f2_pack(nlse[m], nlse[m]);
-                nd2 = f2_pack(ndsum[m], ndsum[m]);
+              for (int m = 0; m < NM; ++m) {
+                uint64_t nl2, nd2;
+                if (kQ) {
+                  nl2 = f2_pack(nlse[m], nlse[m]);
+                  nd2 = f2_pack(ndsum[m], ndsum[m]);
+                } else {
+                  nl2 = nls[m][(k - k4) / 2];
+                  nd2 = nds[m][(k - k4) / 2];
+                }
+                if constexpr (!kDiff) {
+                  const int q = 16 * ch + k;
+                  const uint64_t f2 = f2_pack(f[q / kG], f[(q + 1) / kG]);
+                  const uint64_t c2 = f2_pack(c[q % kG], c[(q + 1) % kG]);
+                  nl2 = kQ ? f2_add(f2, c2) : f2_add(f2_add(f2, c2), nl2);
+                }
+                p2[m] = f2_ex2(f2_fma(
+                    f2_pack(__uint_as_float(x[m][k]), __uint_as_float(x[m][k + 1])), sl2x2, nl2));
+                if (kQ) dfull2[m] = f2_fma(p2[m], e2, dfull2[m]);
+                // (map 2: -lambda is applied to the finished dQ_2 and dK_2)
+                const uint64_t d2 = f2_mul(p2[m], f2_add(e2, nd2));
+                const uint32_t d16 = f2_bf16(d2);
+                ds[m][k / 2] = d16;
+                if (kQ)
+                  rsum2[m] = f2_add(rsum2[m], f2_pack(__uint_as_float(d16 << 16),
+                                                      __uint_as_float(d16 & 0xFFFF0000u)));
+                if constexpr (kTable) {
+                  const int q = 16 * ch + k;
+                  gf2[kG > 1 ? q / kG : q / 2] = f2_add(gf2[kG > 1 ? q / kG : q / 2], d2);
+                  gc2[(q % kG) / 2] = f2_add(gc2[(q % kG) / 2], d2);
+                }
+              }
+              if constexpr (kDiff && !kQ) {
+                pk[0][k / 2] = f2_bf16(f2_fma(nlam2, p2[NM - 1], p2[0]));
               } else {
-                nl2 = nls[m][(k - k4) / 2];
-                nd2 = nds[m][(k - k4) / 2];
-              }
-              if constexpr (!kDiff) {
-                const int q = 16 * ch + k;
-                const uint64_t f2 = f2_pack(f[q / kG], f[(q + 1) / kG]);
-                const uint64_t c2 = f2_pack(c[q % kG], c[(q + 1) % kG]);
-                nl2 = kQ ? f2_add(f2, c2) : f2_add(f2_add(f2, c2), nl2);
-              }
-              p2[m] = f2_ex2(f2_fma(
-                  f2_pack(__uint_as_float(x[m][k]), __uint_as_float(x[m][k + 1])), sl2x2, nl2));
-              if (kQ) dfull2[m] = f2_fma(p2[m], e2, dfull2[m]);
-              // (map 2: -lambda is applied to the finished dQ_2 and dK_2)
-              const uint64_t d2 = f2_mul(p2[m], f2_add(e2, nd2));
-              const uint32_t d16 = f2_bf16(d2);
-              ds[m][k / 2] = d16;
-              if (kQ)
-                rsum2[m] = f2_add(rsum2[m], f2_pack(__uint_as_float(d16 << 16),
-                                                    __uint_as_float(d16 & 0xFFFF0000u)));
-              if constexpr (kTable) {
-                const int q = 16 * ch + k;
-                gf2[kG > 1 ? q / kG : q / 2] = f2_add(gf2[kG > 1 ? q / kG : q / 2], d2);
-                gc2[(q % kG) / 2] = f2_add(gc2[(q % kG) / 2], d2);
-              }
-            }
-            if constexpr (kDiff && !kQ) {
-              pk[0][k / 2] = f2_bf16(f2_fma(nlam2, p2[NM - 1], p2[0]));
-            } else {
 #pragma unroll
-              for (int m = 0; m < NM; ++m) pk[m][k / 2] = f2_bf16(p2[m]);
+                for (int m = 0; m < NM; ++m) pk[m][k / 2] = f2_bf16(p2[m]);
+              }
             }
-          }
           }
         } else {
 #pragma unroll

@@ -429,6 +429,37 @@ def test_other_stream_and_graphs():
     p.check_ok()
 
 
+def test_binding_refuses_wrong_tensors():
+    p = Problem((1, 2, 4, 8, 8, 64, None, False), seed=14, empty=False)
+    q, k, v, g = p.dev()
+    table, bucket, lam = p.table.cuda(), torch.from_numpy(p.bucket).cuda(), p.lam.cuda()
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device="cuda")
+    for mask in (torch.ones(3, 4, 4, dtype=torch.bool), torch.ones(2, 4, 4),
+                 torch.ones(4, 2, 4, dtype=torch.bool).transpose(0, 1)):
+        with pytest.raises(ValueError):
+            api.plan_mask(p.desc, mask.cuda(), p.ws)
+    for t, b, kw in ((table.float(), bucket, {}), (table[:1], bucket, {}), (table, bucket[1:], {}),
+                     (table, bucket.long(), {}), (table, bucket, {"lse": lse[..., 1:]}),
+                     (table, bucket, {"out": q.float()})):
+        with pytest.raises(ValueError):
+            api.fwd_bias(p.desc, q, k, v, t, b, p.ws, **kw)
+    with pytest.raises(ValueError):
+        api.fwd_bias(p.desc, q.transpose(2, 3).contiguous().transpose(2, 3), k, v, table, bucket, p.ws)
+    for kw in ({"lse": lse}, {"out2": q.float()}):
+        with pytest.raises(ValueError):
+            api.fwd_diff(p.desc, q, k, v, lam, p.ws, **kw)
+    with pytest.raises(ValueError):
+        api.fwd_diff(p.desc, q, k, v, lam[:1], p.ws)
+    with pytest.raises(ValueError):
+        api.bwd_bias(p.desc, q, k, v, table, bucket, q, g, lse, p.ws, dtable=table.float())
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(api.SparseAttnError):
+        api.bwd_bias(p.desc, q, k, v, table, bucket, q, g, lse, p.ws, scratch=small)
+    with pytest.raises(api.SparseAttnError):
+        api.plan_mask(p.desc, torch.ones(4, 4, dtype=torch.bool, device="cuda"), small)
+    p.check_ok()
+
+
 def test_bad_bucket_is_reported():
     p = Problem((1, 1, 2, 8, 8, 64, None, True), seed=11, empty=False)
     q, k, v, g = p.dev()
