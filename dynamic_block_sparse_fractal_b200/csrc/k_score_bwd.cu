@@ -339,6 +339,7 @@ __device__ __forceinline__ float f2_sum(uint64_t a) {
 struct SbBars {
   uint64_t tile_full, full[kSbSlots], empty[kSbSlots];
   uint64_t s_full[2], out_full[2], acc_full, dsum_full, drain;
+  uint64_t order;  // nobody waits on it
   uint32_t tmem_base;
   int abort;
 };
@@ -487,6 +488,7 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     mbar_init(&br.acc_full, 1);
     mbar_init(&br.dsum_full, kSbRowWarps);
     mbar_init(&br.drain, 1);
+    mbar_init(&br.order, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -648,7 +650,10 @@ __global__ void __launch_bounds__(kSbThreads, 1)
             mma_from_tmem<W / 16>(tmem + kColY + 64u * m, st + kDP + 8u * m,
                                   b1_mn + where(i) + m * kMap, id_y, acc);
           }
-          if ((i + 1) % kHalves == 0) mma_commit(&br.empty[(i / kHalves) % kSlots]);
+          // A commit stands between the products that read P and dS from TMEM and the
+          // scores that overwrite them in another MMA shape: only MMAs of one shape and
+          // accumulator are ordered by themselves.
+          mma_commit((i + 1) % kHalves == 0 ? &br.empty[(i / kHalves) % kSlots] : &br.order);
           if (more) issue(i + 2);
           const int jn = (i + 3) / kHalves;
           ready = mbar_peek(&br.out_full[(i + 1) & 1], ((i + 1) >> 1) & 1) &&

@@ -317,6 +317,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
           if (one) {
             mma_ts_k<4>(col_o(x), col_s(x, j & 1), v0 + uint64_t(sv) * kSlotStep, id_pv,
                         j > 0 ? 1u : 0u);
+            // (this commit also keeps S_X(j + 2), of another MMA shape, from overwriting
+            // the P that PV_X(j) still reads: without one outputs were wrong at d = 128)
             mma_commit(j + 1 < n ? &sm.pv_done[x] : &sm.o_final[x]);
             if (!kDiff || x == 1) mma_commit(&sm.empty[sv]);
             // The next unit (the other chain's step, or the next one's): its barriers
