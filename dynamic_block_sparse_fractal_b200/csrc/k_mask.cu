@@ -1018,13 +1018,20 @@ cudaError_t launch_mask_bytes(const MaskArgs& a, const uint8_t* mask, size_t hea
 // One CTA per head: bitonic sort of the head's tiles by descending union
 // length, so that the attention grid meets the heaviest tiles of a head first
 // (longest-processing-time order) while concurrently running CTAs still share
-// one head's K/V in L2.
-__global__ void __launch_bounds__(1024) tile_order_kernel(const int32_t* __restrict__ tcnt,
-                                                          int32_t* __restrict__ order, Geometry g) {
-  __shared__ uint32_t key[4096];
-  const int bh = blockIdx.x;
+// one head's K/V in L2. The launch gives a key per slot of the padded sort: a
+// head whose blocks all stand in one column of one frame has a tile per block,
+// 6144 of them, padded to 8192 keys (32 KB).
+static int tile_order_keys(const Geometry& g) {
   int n = 1;
   while (n < g.ntile) n <<= 1;
+  return n;
+}
+
+__global__ void __launch_bounds__(1024) tile_order_kernel(const int32_t* __restrict__ tcnt,
+                                                          int32_t* __restrict__ order, int n,
+                                                          Geometry g) {
+  extern __shared__ uint32_t key[];  // n of them
+  const int bh = blockIdx.x;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     // ascending key = descending count, then ascending tile; padding sorts last
     key[i] = i < g.ntile ? (uint32_t(g.nb - tcnt[size_t(bh) * g.ntile + i]) << 16) | uint32_t(i)
@@ -1053,7 +1060,8 @@ __global__ void __launch_bounds__(1024) tile_order_kernel(const int32_t* __restr
 
 cudaError_t launch_tile_order(const int32_t* tcnt, int32_t* order, const Geometry& g,
                               cudaStream_t stream) {
-  tile_order_kernel<<<unsigned(g.BH), 1024, 0, stream>>>(tcnt, order, g);
+  const int n = tile_order_keys(g);
+  tile_order_kernel<<<unsigned(g.BH), 1024, n * sizeof(uint32_t), stream>>>(tcnt, order, n, g);
   return cudaGetLastError();
 }
 
