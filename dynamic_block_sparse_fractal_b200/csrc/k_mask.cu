@@ -994,6 +994,13 @@ static cudaError_t launch_union_of(const MaskArgs& a, const uint8_t* mask, size_
   int wpc = int((48 * 1024) / warp_bytes);  // warps per CTA within 48 KB
   wpc = wpc < 1 ? 1 : (wpc > kUnionMaxWarps ? kUnionMaxWarps : wpc);
   const unsigned grid = unsigned((items + wpc - 1) / wpc), threads = unsigned(wpc * 32);
+  // one block per frame and nearly 6144 frames: one warp's words alone pass 48 KB
+  static_assert((2 * (6144 / 32 + 1) + 2 * 6144) * sizeof(uint32_t) <= 52 * 1024, "union words");
+  if (wpc * warp_bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        union_kernel<kBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize, 52 * 1024);
+    if (e != cudaSuccess) return e;
+  }
   if constexpr (kBytes)
     return launch_early(union_kernel<true>, grid, threads, wpc * warp_bytes, stream, a, mask,
                         head_stride, order, g);

@@ -1,6 +1,6 @@
-"""Heads with more query tiles than blocks pair up: one frame of blocks in one
-column has a tile per block, so 4,097 to 6,144 tiles a head have to be put in
-order. Every q-block keeps itself and up to two others; the outputs and the
+"""Heads of extreme shape. One frame of blocks in one column has a tile per
+block, so 4,097 to 6,144 tiles a head have to be put in order; one block per
+frame and up to 6,144 frames is the longest list of temporal pairs. Every q-block keeps itself and up to two others; the outputs and the
 gradients of all blocks against fp64, with the bounds of test_gpu_score."""
 import pytest
 import torch
@@ -12,7 +12,8 @@ pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
 
 D = 64
-GRIDS = [((1, 8 * 4097, 8), None), ((1, 8 * 6144, 8), None), ((64, 4500, 1), (64, 1, 1))]
+GRIDS = [((1, 8 * 4097, 8), None), ((1, 8 * 6144, 8), None), ((64, 4500, 1), (64, 1, 1)),
+         ((5957, 8, 8), None), ((6144, 8, 8), None)]
 
 
 class Band:
@@ -59,10 +60,12 @@ class Band:
         assert not bad.any(), f"{name}: {int(bad.sum())} outside"
 
 
-@pytest.mark.parametrize("grid,tile", GRIDS, ids=["4097", "6144", "4500_deep"])
-def test_a_tile_per_block(grid, tile):
+@pytest.mark.parametrize("grid,tile", GRIDS, ids=["4097", "6144", "4500_deep", "5957_frames",
+                                                  "6144_frames"])
+def test_long_heads(grid, tile):
     p = Band(grid, tile, 3)
-    assert api.get_mask(p.desc, p.ws)["tile_cnt"].shape[-1] == p.nb > 4096
+    tiles = p.nb if grid[0] in (1, 64) else (p.nb + 1) // 2
+    assert api.get_mask(p.desc, p.ws)["tile_cnt"].shape[-1] == tiles
     q, k, v, g = p.x
     Q, K, V, G = (p.blocks(t) for t in p.x)
     # plain attention
@@ -107,13 +110,13 @@ def test_a_tile_per_block(grid, tile):
     assert abs(float(dl) - float(want)) <= 2 * E * float((A[1] * dP.abs()).sum()) + 1e-6
 
 
-@pytest.mark.parametrize("nh", [4097, 6144])
-def test_the_plan_of_q_and_k_reaches_every_tile(nh):
+@pytest.mark.parametrize("T,nh", [(1, 4097), (1, 6144), (5958, 1), (6144, 1)])
+def test_the_plan_of_q_and_k_reaches_every_tile(T, nh):
     """Values of 1 give 1 in every row (P is rounded once to bf16 and its sum is not), so a
     tile that no CTA works on shows."""
-    desc = api.make_desc(1, 1, 1, 8 * nh, 8, D, 0.9, out_fp32=True)
+    desc = api.make_desc(1, 1, T, 8 * nh, 8, D, 0.9, out_fp32=True)
     gen = torch.Generator("cuda").manual_seed(nh)
-    q, k = (torch.randn(1, 1, 64 * nh, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    q, k = (torch.randn(1, 1, 64 * T * nh, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
     ws = api.alloc_workspace(desc)
     api.plan(desc, q, k, ws)
     out = torch.full(q.shape, float("nan"), device="cuda")
