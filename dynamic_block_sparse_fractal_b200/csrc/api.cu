@@ -59,7 +59,13 @@ sa_status check_ws(const Geometry& g, const void* ws, size_t ws_bytes) {
   return SA_OK;
 }
 
-sa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SA_OK : SA_ERR_CUDA; }
+// A CUDA call failed: reported by this entry point, and cleared, so that the next
+// one's launch check does not find it again.
+sa_status cuda_failed() {
+  cudaGetLastError();
+  return SA_ERR_CUDA;
+}
+sa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SA_OK : cuda_failed(); }
 
 template <class T>
 T* at(void* base, size_t off) {
@@ -101,13 +107,13 @@ static sa_status plan_impl(const sa_desc* desc, const void* q, const void* k, vo
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
   cudaError_t e;
-  if (ev != nullptr && cudaEventRecord(ev[0], s) != cudaSuccess) return SA_ERR_CUDA;
+  if (ev != nullptr && cudaEventRecord(ev[0], s) != cudaSuccess) return cuda_failed();
   e = cudaMemsetAsync(at<uint32_t>(workspace, w.status), 0, 256, s);
-  if (e != cudaSuccess) return SA_ERR_CUDA;
+  if (e != cudaSuccess) return cuda_failed();
   e = launch_pool(q, k, at<float>(workspace, w.qbar), at<float>(workspace, w.kbar),
                   at<float>(workspace, w.qsplit), at<float>(workspace, w.ksplit), g, s);
-  if (e != cudaSuccess) return SA_ERR_CUDA;
-  if (ev != nullptr && cudaEventRecord(ev[1], s) != cudaSuccess) return SA_ERR_CUDA;
+  if (e != cudaSuccess) return cuda_failed();
+  if (ev != nullptr && cudaEventRecord(ev[1], s) != cudaSuccess) return cuda_failed();
 
   MaskArgs m;
   std::memset(&m, 0, sizeof(m));
@@ -118,7 +124,7 @@ static sa_status plan_impl(const sa_desc* desc, const void* q, const void* k, vo
       !encode_rows_f32(&m.map_qlo, qsplit + rows * g.d, rows, g.d, 128) ||
       !encode_rows_f32(&m.map_khi, ksplit, rows, g.d, 256) ||
       !encode_rows_f32(&m.map_klo, ksplit + rows * g.d, rows, g.d, 256))
-    return SA_ERR_CUDA;
+    return cuda_failed();
   m.status = at<uint32_t>(workspace, w.status);
   m.qbar = at<float>(workspace, w.qbar);
   m.kbar = at<float>(workspace, w.kbar);
@@ -137,11 +143,11 @@ static sa_status plan_impl(const sa_desc* desc, const void* q, const void* k, vo
   m.sta_w = sta ? desc->sta_w / 2 : -1;
   m.scale = (float)(1.0 / std::sqrt((double)g.d));
   e = launch_mask(m, g, s, ev != nullptr ? ev + 2 : nullptr);
-  if (e != cudaSuccess) return SA_ERR_CUDA;
-  if (ev != nullptr && cudaEventRecord(ev[4], s) != cudaSuccess) return SA_ERR_CUDA;
+  if (e != cudaSuccess) return cuda_failed();
+  if (ev != nullptr && cudaEventRecord(ev[4], s) != cudaSuccess) return cuda_failed();
   e = launch_tile_order(m.tcnt, at<int32_t>(workspace, w.order), g, s);
-  if (e != cudaSuccess) return SA_ERR_CUDA;
-  if (ev != nullptr && cudaEventRecord(ev[5], s) != cudaSuccess) return SA_ERR_CUDA;
+  if (e != cudaSuccess) return cuda_failed();
+  if (ev != nullptr && cudaEventRecord(ev[5], s) != cudaSuccess) return cuda_failed();
   return SA_OK;
 }
 
@@ -163,13 +169,13 @@ sa_status sparse_attn_plan_profile(const sa_desc* desc, const void* q, const voi
   int made = 0;
   for (; made <= kNumPlanStages; ++made)
     if (cudaEventCreate(&ev[made]) != cudaSuccess) break;
-  st = made == kNumPlanStages + 1 ? SA_OK : SA_ERR_CUDA;
+  st = made == kNumPlanStages + 1 ? SA_OK : cuda_failed();
   for (int r = 0; r < reps && st == SA_OK; ++r) {
     st = plan_impl(desc, q, k, workspace, ws_bytes, stream, ev);
-    if (st == SA_OK && cudaEventSynchronize(ev[kNumPlanStages]) != cudaSuccess) st = SA_ERR_CUDA;
+    if (st == SA_OK && cudaEventSynchronize(ev[kNumPlanStages]) != cudaSuccess) st = cuda_failed();
     for (int i = 0; i < kNumPlanStages && st == SA_OK; ++i) {
       float ms = 0.f;
-      if (cudaEventElapsedTime(&ms, ev[i], ev[i + 1]) != cudaSuccess) st = SA_ERR_CUDA;
+      if (cudaEventElapsedTime(&ms, ev[i], ev[i + 1]) != cudaSuccess) st = cuda_failed();
       stage_us[i] += ms * 1000.f / float(reps);
     }
   }
@@ -211,7 +217,7 @@ static sa_status fwd_impl(const sa_desc* desc, const void* q, const void* k, con
       !encode_tile_map(&a.map_v, v, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
       !encode_tile_map(&a.map_k2, k, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw, pair_frames) ||
       !encode_tile_map(&a.map_v2, v, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw, pair_frames))
-    return SA_ERR_CUDA;
+    return cuda_failed();
   a.out = out;
   a.tcnt = at<int32_t>(workspace, w.tcnt);
   a.tidx = at<int32_t>(workspace, w.tidx);
@@ -268,7 +274,7 @@ sa_status sparse_attn_bwd(const sa_desc* desc, const void* q, const void* k, con
       !encode_tile_map(&a.map_k, k, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
       !encode_tile_map(&a.map_v, v, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
       !encode_tile_map(&a.map_do, dout, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw))
-    return SA_ERR_CUDA;
+    return cuda_failed();
   a.lse2 = at<float>(scratch, b.lse2);
   a.dsum = at<float>(scratch, b.dsum);
   a.kcnt = at<int32_t>(scratch, b.kcnt);
@@ -318,14 +324,14 @@ sa_status sparse_attn_block_heatmap(const sa_desc* desc, const void* q, const vo
   std::memset(&a, 0, sizeof(a));
   if (!encode_tile_map(&a.map_q, q, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
       !encode_tile_map(&a.map_k, k, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw))
-    return SA_ERR_CUDA;
+    return cuda_failed();
   a.heat = heat;
   a.scratch = static_cast<float*>(scratch);
   a.status = at<uint32_t>(workspace, w.status);
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)g.d));
   a.debug_flags = desc->debug_flags;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s) != cudaSuccess) return SA_ERR_CUDA;
+  if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s) != cudaSuccess) return cuda_failed();
   return cuda_status(launch_heat(a, g, s));
 }
 
@@ -345,13 +351,13 @@ sa_status sparse_attn_token_entropy(const sa_desc* desc, const void* q, const vo
   std::memset(&a, 0, sizeof(a));
   if (!encode_tile_map(&a.map_q, q, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
       !encode_tile_map(&a.map_k, k, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw))
-    return SA_ERR_CUDA;
+    return cuda_failed();
   a.entropy = entropy;
   a.status = at<uint32_t>(workspace, w.status);
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)g.d));
   a.debug_flags = desc->debug_flags;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s) != cudaSuccess) return SA_ERR_CUDA;
+  if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s) != cudaSuccess) return cuda_failed();
   return cuda_status(launch_heat(a, g, s));
 }
 
@@ -372,7 +378,7 @@ sa_status sparse_attn_plan_radius(const sa_desc* desc, const sa_radius* radius,
   const WsLayout w = make_ws_layout(g);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(at<uint32_t>(workspace, w.status), 0, 256, s) != cudaSuccess)
-    return SA_ERR_CUDA;
+    return cuda_failed();
   RadiusArgs r;
   r.entropy = entropy;
   r.bits = at<uint32_t>(workspace, w.bits);
@@ -381,7 +387,7 @@ sa_status sparse_attn_plan_radius(const sa_desc* desc, const sa_radius* radius,
   r.tau = radius->tau;
   r.gamma = radius->gamma;
   r.vote_min = radius->vote_min;
-  if (launch_radius(r, g, s) != cudaSuccess) return SA_ERR_CUDA;
+  if (launch_radius(r, g, s) != cudaSuccess) return cuda_failed();
   MaskArgs m;
   std::memset(&m, 0, sizeof(m));
   m.bits = r.bits;
@@ -390,7 +396,7 @@ sa_status sparse_attn_plan_radius(const sa_desc* desc, const sa_radius* radius,
   m.tcnt = at<int32_t>(workspace, w.tcnt);
   m.tidx = at<int32_t>(workspace, w.tidx);
   m.status = at<uint32_t>(workspace, w.status);
-  if (launch_union(m, g, s) != cudaSuccess) return SA_ERR_CUDA;
+  if (launch_union(m, g, s) != cudaSuccess) return cuda_failed();
   return cuda_status(launch_tile_order(m.tcnt, at<int32_t>(workspace, w.order), g, s));
 }
 
@@ -434,7 +440,7 @@ static sa_status score_fwd_impl(const sa_desc* desc, const BiasArgs& bias, const
   if (!encode_tile_map(&a.map_q, q, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
       !encode_tile_map(&a.map_k, k, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
       !encode_tile_map(&a.map_v, v, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw))
-    return SA_ERR_CUDA;
+    return cuda_failed();
   a.out = out;
   a.out2 = out2;
   a.lse = lse;
@@ -506,7 +512,7 @@ static sa_status score_bwd_impl(const sa_desc* desc, const BiasArgs& bias, const
       !encode_tile_map(&a.map_k, k, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
       !encode_tile_map(&a.map_v, v, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw) ||
       !encode_tile_map(&a.map_do, dout, g.BH, g.T, g.Hh, g.Ww, g.d, g.pt, g.ph, g.pw))
-    return SA_ERR_CUDA;
+    return cuda_failed();
   a.out = out;
   a.out2 = out2;
   a.dout = static_cast<const __nv_bfloat16*>(dout);
@@ -632,12 +638,12 @@ sa_status sparse_attn_check(const sa_desc* desc, const void* workspace, size_t w
   st = check_ws(g, workspace, ws_bytes);
   if (st != SA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaStreamSynchronize(s) != cudaSuccess) return SA_ERR_CUDA;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return cuda_failed();
   uint32_t word = 0;
   const WsLayout w = make_ws_layout(g);
   if (cudaMemcpy(&word, at<uint32_t>(workspace, w.status), sizeof(word), cudaMemcpyDeviceToHost) !=
       cudaSuccess)
-    return SA_ERR_CUDA;
+    return cuda_failed();
   return word ? SA_ERR_DEVICE_TIMEOUT : SA_OK;
 }
 
