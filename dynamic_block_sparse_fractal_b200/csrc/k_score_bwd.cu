@@ -213,13 +213,8 @@ __device__ __forceinline__ int lane_sums(float (&v)[N], int lane, int& first, bo
 
 // dS of this thread's key against 32 query columns of a block, already summed
 // over each run (f) and each column (c), added to the warp's own histogram over
-// offsets (t, h, w: the block's indexes in it). Lanes of a warp are 32 tokens of
-// one block: their low L bits are the column. Lanes that share an address sum
-// first; then one group of lanes at a time adds, whose addresses all differ, so
-// that no atomics are needed (histograms shared by the CTA's warps with atomic
-// additions took 4,500 cycles a step, three times the step's products). Blocks
-// of several frames can still meet at an address and add atomically.
-// The same for blocks of one frame with rows of 8 (the 8 x 8 patch). A warp holds
+// offsets (h, w: the block's indexes in it), for blocks of one frame with rows of
+// 8 (the 8 x 8 patch); add_table_grad below is the same for the others. A warp holds
 // 4 rows x 8 columns of keys against 4 rows x 8 columns of queries: 1 + 7 + 15
 // offsets. The sums over one axis are brought together along their diagonals by
 // shuffles, so that one addition to the histogram, each lane at an address of its
@@ -265,6 +260,14 @@ __device__ __forceinline__ void add_table_grad_patch(float* hist, int h, int w, 
   __syncwarp();
 }
 
+// The same for any block shape (t, h, w: the block's indexes in the histogram).
+// Lanes of a warp are 32 tokens of one block: their low L bits are the column.
+// Lanes that share an address sum first; then one group of lanes at a time adds
+// one of its values, at addresses that all differ, so that no atomics are needed
+// (histograms shared by the CTA's warps with atomic additions took 4,500 cycles a
+// step, three times the step's products). A lane's next value meets its
+// neighbour's last address: the warp synchronises between values. Blocks of
+// several frames can still meet at an address and add atomically.
 template <int L>
 __device__ __forceinline__ void add_table_grad(float* hist, const Geometry& g, int t, int h, int w,
                                                int wg, int lane, float (&f)[Cols<L>::kF],
@@ -285,12 +288,13 @@ __device__ __forceinline__ void add_table_grad(float* hist, const Geometry& g, i
     // lanes of equal column bits are different rows of the block
     constexpr int kStep = NF >= 1 << L ? 1 : (1 << L) / NF;  // (the others are no writers)
     for (int q = 0; q < 1 << L; q += kStep) {
-      if (writer && (lane & ((1 << L) - 1)) == q) {
+      const bool mine = writer && (lane & ((1 << L) - 1)) == q;
 #pragma unroll
-        for (int k = 0; k < NF; ++k)
-          if (k < n) hist[h - (f_run<L>(g, wg, first + k) & (g.ph - 1))] += f[k];
+      for (int k = 0; k < NF; ++k) {
+        if (k >= n) break;
+        if (mine) hist[h - (f_run<L>(g, wg, first + k) & (g.ph - 1))] += f[k];
+        __syncwarp();
       }
-      __syncwarp();
     }
   } else if (writer) {
 #pragma unroll
@@ -305,12 +309,13 @@ __device__ __forceinline__ void add_table_grad(float* hist, const Geometry& g, i
   n = lane_sums<NG, L, 5>(c, lane, first, writer);  // lanes of one column
 #pragma unroll
   for (int q = 0; q < 32 >> L; ++q) {  // lanes of one row run: different columns
-    if (writer && (lane >> L) == q) {
+    const bool mine = writer && (lane >> L) == q;
 #pragma unroll
-      for (int k = 0; k < NG; ++k)
-        if (k < n) hist[w - g_col<L>(g, wg, first + k)] += c[k];
+    for (int k = 0; k < NG; ++k) {
+      if (k >= n) break;
+      if (mine) hist[w - g_col<L>(g, wg, first + k)] += c[k];
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
