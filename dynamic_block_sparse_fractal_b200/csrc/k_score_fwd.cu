@@ -16,16 +16,20 @@
 // this takes 1.68 (differential, 4 heads of 61,440 tokens) and 1.82 ms where this
 // takes 1.45 (bias, 12 x 37,632).
 //
-//   warps 0, 2, 3  TMA producers, one 16 KB ring slot per block of K or V, in the
-//                  order the MMA warp consumes them; the maps share their slots
-//   warp 1         issues, from one elected lane, a unit per chain and step:
-//                  PV_X(j), then S_X(j + 2) into the stage that frees
+//   warps 0, 2     TMA producers, one 16 KB ring slot per block of K or V, in the
+//                  order the MMA warps consume them: a ring per chain (bias), or one
+//                  that the maps share
+//   warps 1, 3     one issues A's products and the other B's, a step at a time:
+//                  PV_X(j), then S_X(j + 2) into the stage that it frees
 //   warps 4-7, 8-11  softmax of chain A and B, one thread per query row
 //
-// MMAs issued by one thread run in order and a commit tracks every earlier one,
-// so S_X(j) complete means PV_X(j - 2) is; a rescale of O at step j waits for
-// PV_X(j - 1). All waits are bounded; one that runs out records a status bit and
-// raises the CTA's abort flag.
+// S_X(j + 2) overwrites the P of step j. Only MMAs of one shape and accumulator are
+// ordered by being issued one after the other, so it goes out after PV_X(j)'s commit
+// has arrived; the other chain's products fill that wait, which is why the chains
+// have a warp each (one warp for both, waiting: 250 and 350 us where two take 208
+// and 290; bias and differential, 12 x 8,192 tokens). So S_X(j) complete means
+// PV_X(j - 2) is; a rescale of O at step j waits for PV_X(j - 1). All waits are
+// bounded; one that runs out records a status bit and raises the CTA's abort flag.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -40,7 +44,6 @@ namespace {
 
 constexpr int kFThreads = 384;
 constexpr int kFSlots = 8;
-constexpr int kFProducers = 3;
 constexpr int kFTile = 128 * 128;  // 128 rows x 128 B (64 bf16 channels)
 constexpr int kFBlk = 64 * 128;    // 64 rows x 128 B
 constexpr int kFList = 2880;       // union entries staged per chain (the rest from L2)
@@ -53,13 +56,25 @@ struct __align__(1024) ScoreFwdSmem {
   int32_t list[2][kFList];
   float m[2][128], l[2][128];  // row statistics of A and B where their outputs join
   uint64_t q_full[2], full[kFSlots], empty[kFSlots];
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_final[2], join, drain;
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_final[2], join, drain[2];
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(ScoreFwdSmem<128>) + 1024 + sizeof(float) * (2 * kRelBiasMaxAxes - 3) <=
                   232448,
               "shared memory of the forward");
+
+// Slot of ring position k: the differential chains share a ring of all slots, the
+// others have half of them each.
+template <bool kShared>
+__device__ __forceinline__ int ring_slot(int x, int k) {
+  return kShared ? k % kFSlots : x * (kFSlots / 2) + k % (kFSlots / 2);
+}
+
+template <int V>
+struct Which {
+  static constexpr int value = V;
+};
 
 struct Chain {
   int qa, qb;            // q-blocks (qb = -1: lone block)
@@ -124,6 +139,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   constexpr bool kDiff = M == AttnMode::kDiff, kRows = !kDiff && L != kAnyShape;
   const bool split = !kDiff && a.split;
   const bool one_tile = kDiff || split;
+  constexpr int kRing = kDiff ? kFSlots : kFSlots / 2;
   extern __shared__ uint8_t sf_raw[];
   // (an offset, not an address rounded up: the compiler then knows shared memory)
   ScoreFwdSmem<D>& sm =
@@ -146,10 +162,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
     }
     for (int s = 0; s < kFSlots; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.empty[s], kDiff ? 2 : 1);  // the maps share a slot
     }
     mbar_init(&sm.join, 256);
-    mbar_init(&sm.drain, 1);
+    for (int x = 0; x < 2; ++x) mbar_init(&sm.drain[x], 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -189,9 +205,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
   auto col_s = [&](int x, int st) { return tmem + 128u * x + 64u * st; };
   auto col_o = [&](int x) { return tmem + 256u + 128u * x; };
 
-  if (warp < 4 && warp != 1) {
+  if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ producers
-    const int prod = warp == 0 ? 0 : warp - 1;  // 0, 1, 2: every third slot each
+    // bias: warp 0 fills A's ring and warp 2 B's; the maps share one ring of all slots
+    // and the warps take turns. A ring's order is K(0), K(1), then V(j), K(j + 2).
+    const int prod = warp >> 1;
     if (lane == 0) {
       if (prod == 0) {
         prefetch_tensormap(&a.map_q);
@@ -211,15 +229,20 @@ __global__ void __launch_bounds__(kFThreads, 1)
           }
         }
       }
+      const Chain c = !kDiff && prod == 1 ? chain[1] : chain[0];
       int k = 0, last = -1;
       bool ok = true;
-      auto load = [&](const CUtensorMap* map, int x, int j) {  // the ring's next slot
-        const int s = k % kFSlots, use = k / kFSlots;
-        if (k++ % kFProducers != prod || !ok) return;
-        ok = (use == 0 || mbar_wait(&sm.empty[s], (use - 1) & 1, abort)) && !*abort;
+      auto load = [&](const CUtensorMap* map, int j) {  // the ring's next slot
+        const int s = ring_slot<kDiff>(prod, k), use = k / kRing;
+        if (kDiff && (k & 1) != prod) {
+          ++k;
+          return;
+        }
+        ++k;
+        ok = ok && (use == 0 || mbar_wait(&sm.empty[s], (use - 1) & 1, abort)) && !*abort;
         if (!ok) return;
         if (k == 1 && (a.debug_flags & SA_DEBUG_STALL_LOADER)) return;  // test hook
-        int kb = (x ? chain[1] : chain[0]).at(j) & kEntryBlockMask;
+        int kb = c.at(j) & kEntryBlockMask;
         if (kb >= g.nb) {
           atomicOr(a.status, kDevErrBadIndex);
           kb = 0;
@@ -227,21 +250,15 @@ __global__ void __launch_bounds__(kFThreads, 1)
         int t, hp, wp;
         block_coords(g, kb, t, hp, wp);
         mbar_arrive_expect_tx(&sm.full[s], 64u * D * 2u);
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_5d(&sm.slot[s][c][0], map, &sm.full[s], c * 64, wp * g.pw, hp * g.ph, t * g.pt,
-                      bh);
+        for (int ch = 0; ch < D / 64; ++ch)
+          tma_load_5d(&sm.slot[s][ch][0], map, &sm.full[s], ch * 64, wp * g.pw, hp * g.ph,
+                      t * g.pt, bh);
         last = k - 1;
       };
-      const int na = chain[0].n, nb_ = kDiff ? 0 : chain[1].n, nmax = na > nb_ ? na : nb_;
-      for (int j = 0; j < 2; ++j) {
-        if (j < na) load(&a.map_k, 0, j);
-        if (j < nb_) load(&a.map_k, 1, j);
-      }
-      for (int j = 0; ok && j < nmax; ++j) {
-        if (j < na) load(&a.map_v, 0, j);
-        if (j + 2 < na) load(&a.map_k, 0, j + 2);
-        if (j < nb_) load(&a.map_v, 1, j);
-        if (j + 2 < nb_) load(&a.map_k, 1, j + 2);
+      for (int j = 0; j < 2 && j < c.n; ++j) load(&a.map_k, j);
+      for (int j = 0; ok && j < c.n; ++j) {
+        load(&a.map_v, j);
+        if (j + 2 < c.n) load(&a.map_k, j + 2);
       }
       if (!ok) {
         fail_f(a.status, &sm.abort, kDevErrTimeoutLoad);
@@ -250,26 +267,26 @@ __global__ void __launch_bounds__(kFThreads, 1)
         // let this warp's own copies land before the CTA can exit (time-bounded,
         // ignoring the abort flag); at most one per slot is still in flight
         int never = 0;
-        for (int kk = last; kk >= 0 && kk > last - kFSlots; kk -= kFProducers)
-          mbar_wait(&sm.full[kk % kFSlots], (kk / kFSlots) & 1, &never);
+        for (int kk = last; kk >= 0 && kk > last - kRing; kk -= kDiff ? 2 : 1)
+          mbar_wait(&sm.full[ring_slot<kDiff>(prod, kk)], (kk / kRing) & 1, &never);
       }
     }
-  } else if (warp == 1) {
+  } else if (warp < 4) {
     // ------------------------------------------------------------------ MMA
-    const int na = __shfl_sync(0xFFFFFFFFu, chain[0].n, 0);
-    const int nb_ = __shfl_sync(0xFFFFFFFFu, chain[1].n, 0);
-    const int nmax = na > nb_ ? na : nb_;
-    if (nmax > 0) {
+    auto issue_chain = [&](auto which) {  // warp 1: chain 0 (A), warp 3: chain 1 (B)
+      constexpr int x = decltype(which)::value;
+      const int n = __shfl_sync(0xFFFFFFFFu, chain[x].n, 0);
+      if (n == 0) return;
       constexpr uint32_t id_s = idesc_bf16_f32(128, 64, 0, 0);
       constexpr uint32_t id_pv = idesc_bf16_f32(128, D, 0, 1);
       constexpr uint32_t kSlotStep = (D / 64) * kFBlk / 16;
-      const uint64_t q0 = sw128_desc(smem_u32(&sm.q[0][0][0]), 16, 1024);
-      const uint64_t q1 = one_tile ? q0 : sw128_desc(smem_u32(&sm.q[1][0][0]), 16, 1024);
+      const int qt = one_tile ? 0 : x;
+      const uint64_t q = sw128_desc(smem_u32(&sm.q[qt][0][0]), 16, 1024);
       const uint64_t k0 = sw128_desc(smem_u32(&sm.slot[0][0][0]), 16, 1024);
       const uint64_t v0 = sw128_desc(smem_u32(&sm.slot[0][0][0]), kFBlk, 1024);
       const bool one = elect_one();
-      auto mma_s = [&](int x, int j, int s) {  // S_X(j), the K block in slot s
-        const uint64_t q = x ? q1 : q0, k = k0 + uint64_t(s) * kSlotStep;
+      auto mma_s = [&](int j, int s) {  // S_X(j), the K block in slot s
+        const uint64_t k = k0 + uint64_t(s) * kSlotStep;
         constexpr int kSteps = kDiff ? D / 32 : D / 16;
 #pragma unroll
         for (int kk = 0; kk < kSteps; ++kk) {
@@ -279,76 +296,53 @@ __global__ void __launch_bounds__(kFThreads, 1)
                  k + ((uint32_t(ks >> 2) * kFBlk + in) >> 4), id_s, kk > 0);
         }
         mma_commit(&sm.s_full[x][j & 1]);
-        if (!kDiff || x == 1) mma_commit(&sm.empty[s]);
+        mma_commit(&sm.empty[s]);
       };
-      bool ok = (na == 0 || mbar_wait(&sm.q_full[0], 0, abort)) &&
-                (one_tile || nb_ == 0 || mbar_wait(&sm.q_full[1], 0, abort));
+      bool ok = mbar_wait(&sm.q_full[qt], 0, abort);
       int k = 0;  // ring position
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (j >= (x ? nb_ : na)) continue;
-          ok = ok && mbar_wait(&sm.full[k % kFSlots], (k / kFSlots) & 1, abort);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          tc_fence_after_sync();
-          if (ok && one) mma_s(x, j, k % kFSlots);
-          __syncwarp();
-          if (!kDiff || x == 1) ++k;
-        }
+      for (int j = 0; j < 2 && j < n; ++j, ++k) {
+        const int sk = ring_slot<kDiff>(x, k);
+        ok = ok && mbar_wait(&sm.full[sk], 0, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after_sync();
+        if (ok && one) mma_s(j, sk);
+        __syncwarp();
       }
-      bool ready = false;  // the issuing lane's look at the next unit's barriers
-      for (int j = 0; ok && j < nmax; ++j) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int n = x ? nb_ : na;
-          if (!ok || j >= n) continue;
-          const bool has_s = j + 2 < n;
-          const int sv = k % kFSlots, sk = (k + 1) % kFSlots;
-          const uint32_t pv_par = (k / kFSlots) & 1, pk_par = ((k + 1) / kFSlots) & 1;
-          if (!__any_sync(0xFFFFFFFFu, ready)) {
-            ok = mbar_wait(&sm.p_full[x][j & 1], (j >> 1) & 1, abort) &&
-                 mbar_wait(&sm.full[sv], pv_par, abort) &&
-                 (!has_s || mbar_wait(&sm.full[sk], pk_par, abort));
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-          }
+      for (int j = 0; ok && j < n; ++j) {
+        const bool has_s = j + 2 < n;
+        const int sv = ring_slot<kDiff>(x, k), sk = ring_slot<kDiff>(x, k + 1);
+        ok = mbar_wait(&sm.p_full[x][j & 1], (j >> 1) & 1, abort) &&
+             mbar_wait(&sm.full[sv], (k / kRing) & 1, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (one) {
+          mma_ts_k<4>(col_o(x), col_s(x, j & 1), v0 + uint64_t(sv) * kSlotStep, id_pv,
+                      j > 0 ? 1u : 0u);
+          mma_commit(j + 1 < n ? &sm.pv_done[x] : &sm.o_final[x]);
+          mma_commit(&sm.empty[sv]);
+        }
+        __syncwarp();
+        if (has_s) {  // PV_X(j) has to be done with the P that S_X(j + 2) overwrites
+          ok = mbar_wait(&sm.full[sk], ((k + 1) / kRing) & 1, abort) &&
+               mbar_wait(&sm.pv_done[x], j & 1, abort);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
           tc_fence_after_sync();
-          const int k_next = k + (!kDiff || x == 1 ? (has_s ? 2 : 1) : 0);
-          if (one) {
-            mma_ts_k<4>(col_o(x), col_s(x, j & 1), v0 + uint64_t(sv) * kSlotStep, id_pv,
-                        j > 0 ? 1u : 0u);
-            // (this commit also keeps S_X(j + 2), of another MMA shape, from overwriting
-            // the P that PV_X(j) still reads: without one outputs were wrong at d = 128)
-            mma_commit(j + 1 < n ? &sm.pv_done[x] : &sm.o_final[x]);
-            if (!kDiff || x == 1) mma_commit(&sm.empty[sv]);
-            // The next unit (the other chain's step, or the next one's): its barriers
-            // are looked at between this unit's products, since a shared-memory access
-            // waits for the MMAs issued before it (at a unit's end it left the tensor
-            // core idle for 250 of 770 cycles).
-            const int xn = x == 0 && j < nb_ ? 1 : (j + 1 < na ? 0 : 1);
-            const int jn = xn == 1 && x == 0 ? j : j + 1;
-            const int nn = xn ? nb_ : na;
-            ready = false;
-            if (jn < nn) {
-              const int s1 = k_next % kFSlots, s2 = (k_next + 1) % kFSlots;
-              const uint32_t par1 = (k_next / kFSlots) & 1, par2 = ((k_next + 1) / kFSlots) & 1;
-              ready = mbar_peek3(&sm.p_full[xn][jn & 1], (jn >> 1) & 1, &sm.full[s1], par1,
-                                 jn + 2 < nn ? &sm.full[s2] : &sm.full[s1],
-                                 jn + 2 < nn ? par2 : par1) == 7u;
-            }
-            if (has_s) mma_s(x, j + 2, sk);
-          }
-          k = k_next;
+          if (one) mma_s(j + 2, sk);
           __syncwarp();
         }
+        k += has_s ? 2 : 1;
       }
       if (!ok) {
         fail_f(a.status, &sm.abort, kDevErrTimeoutMma);
-        if (one) mma_commit(&sm.drain);  // wait for the in-flight MMAs
+        if (one) mma_commit(&sm.drain[x]);  // wait for the in-flight MMAs
         int never = 0;
-        mbar_wait(&sm.drain, 0, &never);
+        mbar_wait(&sm.drain[x], 0, &never);
       }
-    }
+    };
+    if (warp == 1) issue_chain(Which<0>{});
+    else issue_chain(Which<1>{});
   } else {
     // -------------------------------------------------------------- softmax
     const int x = (warp - 4) >> 2;

@@ -1,10 +1,12 @@
-"""The table's gradient of every block shape: the shapes of one frame against the
-oracle and bit for bit the same at every run, the others against the oracle (bounds
-and problems of test_gpu_score)."""
+"""Every block shape, and lists of unequal length. The table's gradient: shapes of
+one frame against the oracle and bit for bit the same at every run, the others
+against the oracle (bounds and problems of test_gpu_score)."""
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_score import Problem, check_bias, run_bias
+from dynamic_block_sparse_fractal_b200 import api
+from tests.test_gpu_score import Problem, check_bias, check_diff, run_bias
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
@@ -39,3 +41,27 @@ def test_same_bits_of_every_shape_of_one_frame(tile):
     for _ in range(20):
         again = run_bias(p, q, k, v, g, table, bucket)
         assert all(torch.equal(a, b) for a, b in zip(first[:2] + first[2], again[:2] + again[2]))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_chains_of_unequal_length(d):
+    """More than four tiles per SM, two tiles a head: CTAs whose two tiles have 0 to 12
+    steps, in every pairing of a short and a long list."""
+    H = 100
+    p = Problem((1, H, 2, 8, 48, d, None, False), seed=23)  # 12 blocks, 6 tiles
+    sizes = [0, 1, 2, 3, 4, 12]
+    for h in range(H):
+        p.mask[h] = False
+        for tile in range(6):
+            a, b = tile, tile + 6  # a frame's block and the next one's
+            n = sizes[(h + tile * (1 + h // 6 % 5)) % 6]
+            keep = np.random.default_rng(100 * h + tile).permutation(12)[:n]
+            p.mask[h, a, keep] = True
+            p.mask[h, b, keep[: n // 2 + 1]] = True
+    q, k, v, g = p.dev()
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device="cuda")
+    out = api.fwd_bias(p.desc, q, k, v, p.table.cuda(), torch.from_numpy(p.bucket).cuda(), p.ws, lse=lse)
+    out_d = api.fwd_diff(p.desc, q, k, v, p.lam.cuda(), p.ws)
+    p.check_ok()
+    check_bias(p, out, lse)
+    check_diff(p, out_d, None, None)
