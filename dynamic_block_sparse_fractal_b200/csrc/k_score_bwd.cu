@@ -41,7 +41,7 @@ namespace sa {
 
 namespace {
 
-constexpr int kSbThreads = 640;   // warps 0, 2 TMA, 1 MMA, 3 idle; 4-19 rows
+constexpr int kSbThreads = 640;   // warps 0, 2 TMA, 1, 3 MMA; 4-19 rows
 constexpr int kSbRowWarps = 16;   // two groups of 8: the even and the odd steps; in a group two
                                   // warpgroups of 128 rows, half of a step's columns each
 constexpr int kSbList = 2880;     // list entries staged in shared memory (the rest from L2)
@@ -343,8 +343,7 @@ __device__ __forceinline__ float f2_sum(uint64_t a) {
 // What a CTA of either pass streams and waits on.
 struct SbBars {
   uint64_t tile_full, full[kSbSlots], empty[kSbSlots];
-  uint64_t s_full[2], out_full[2], acc_full, dsum_full, drain;
-  uint64_t order;  // nobody waits on it
+  uint64_t s_full[2], out_full[2], x_done[2], y_done[2], acc_full, dsum_full, drain[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -489,11 +488,12 @@ __global__ void __launch_bounds__(kSbThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&br.s_full[s], 1);
       mbar_init(&br.out_full[s], kSbRowWarps / 2);
+      mbar_init(&br.x_done[s], 1);
+      mbar_init(&br.y_done[s], 1);
+      mbar_init(&br.drain[s], 1);
     }
     mbar_init(&br.acc_full, 1);
     mbar_init(&br.dsum_full, kSbRowWarps);
-    mbar_init(&br.drain, 1);
-    mbar_init(&br.order, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -587,10 +587,16 @@ __global__ void __launch_bounds__(kSbThreads, 1)
           mbar_wait(&br.full[jj % kSlots], (jj / kSlots) & 1, &never);
       }
     }
-  } else if (warp == 1) {
+  } else if (warp < 4) {
     // ------------------------------------------------------------------ MMA
-    // The whole warp walks the steps, so that the loop's values are uniform (the
-    // descriptors stay in uniform registers); one elected lane issues.
+    // Warp 3 issues a step's scores, warp 1 its products X and Y. The scores of step i
+    // overwrite the P and dS that X and Y of step i - 2 read, in another MMA shape, and
+    // only MMAs of one shape and accumulator are ordered by being issued one after the
+    // other: S waits for X to have completed and dP for Y, while the products of step
+    // i - 1 go out beside that wait. (One commit for X and Y together: 1,040 us where
+    // this takes 980, differential, 12 x 8,192 tokens.) Each warp walks the steps as a
+    // whole, so that the loop's values are uniform (the descriptors stay in uniform
+    // registers); one elected lane issues.
     if (nblk > 0) {
       constexpr uint32_t id_s = idesc_bf16_f32(128, W, 0, 0);
       constexpr uint32_t id_y = idesc_bf16_f32(128, kDiff ? 64 : D, 0, 1);
@@ -598,81 +604,80 @@ __global__ void __launch_bounds__(kSbThreads, 1)
       constexpr uint32_t kSlot = (D / 64) * kBlk / 16;   // a slot in descriptor units
       constexpr uint32_t kHalf = W * 128 / 16;           // W rows of a block
       constexpr uint32_t kMap = D == 128 ? kBlk / 16 : 0;  // a map's channels of a block
-      const uint64_t a1 = sw128_desc(smem_u32(&sm.ta[0][0]), 16, 1024);
-      const uint64_t a2 = sw128_desc(smem_u32(&sm.tb[0][0]), 16, 1024);
       const uint64_t b1 = sw128_desc(smem_u32(&sm.sa[0][0][0]), 16, 1024);
       const uint64_t b2 = sw128_desc(smem_u32(&sm.sb[0][0][0]), 16, 1024);
-      const uint64_t b1_mn = sw128_desc(smem_u32(&sm.sa[0][0][0]), kBlk, 1024);
-      const uint64_t b2_mn = sw128_desc(smem_u32(&sm.sb[0][0][0]), kBlk, 1024);
       auto where = [&](int i) -> uint64_t {
         return uint64_t((i / kHalves) % kSlots) * kSlot + uint64_t(i % kHalves) * kHalf;
       };
-      const bool one = elect_one();
-      auto issue = [&](int i) {  // S and dP of step i
-        const uint32_t st = tmem + kStage0 + kStage * uint32_t(i & 1);
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-          mma_scores<D / 16 / NM>(st + W * m, a1, kTile, b1 + where(i), kBlk, id_s,
-                                  m * (D / 16 / NM));
-        mma_scores<D / 16>(st + kDP, a2, kTile, b2 + where(i), kBlk, id_s, 0);
-        mma_commit(&br.s_full[i & 1]);
+      auto block_here = [&](int i) {  // the streamed block of step i
+        const int j = i / kHalves;
+        return i % kHalves != 0 || mbar_wait(&br.full[j % kSlots], (j / kSlots) & 1, abort);
       };
-      bool ok = mbar_wait(&br.tile_full, 0, abort) && mbar_wait(&br.full[0], 0, abort);
-      if (kHalves == 1 && n > 1) ok = ok && mbar_wait(&br.full[1 % kSlots], 0, abort);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (ok) {
-        tc_fence_after_sync();
-        if (one) {
-          issue(0);
-          if (n > 1) issue(1);
-        }
-        __syncwarp();
-      }
-      // One unit per step: X and Y of step i, then S and dP of step i + 2 into the
-      // stage that they free, behind one round of waits. The issuing lane looks at
-      // the next unit's barriers while this unit's products are in the queue.
-      bool ready = false;
-      for (int i = 0; ok && i < n; ++i) {
-        const bool more = i + 2 < n;
-        const int j = (i + 2) / kHalves;
-        if (!__any_sync(0xFFFFFFFFu, ready)) {
-          ok = mbar_wait(&br.out_full[i & 1], (i >> 1) & 1, abort) &&
-               (!more || mbar_wait(&br.full[j % kSlots], (j / kSlots) & 1, abort));
+      const bool one = elect_one();
+      bool ok = true;
+      if (warp == 3) {
+        const uint64_t a1 = sw128_desc(smem_u32(&sm.ta[0][0]), 16, 1024);
+        const uint64_t a2 = sw128_desc(smem_u32(&sm.tb[0][0]), 16, 1024);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&br.tile_full, 0, abort));
+        for (int i = 0; ok && i < n; ++i) {  // S and dP of step i
+          const uint32_t before = ((i >> 1) - 1) & 1;  // the stage's last step
+          ok = block_here(i) && (i < 2 || mbar_wait(&br.x_done[i & 1], before, abort));
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
-        }
-        tc_fence_after_sync();
-        if (one) {
+          tc_fence_after_sync();
           const uint32_t st = tmem + kStage0 + kStage * uint32_t(i & 1);
-          const uint32_t acc = i > 0 ? 1u : 0u;
+          if (one) {
 #pragma unroll
-          for (int m = 0; m < NM; ++m) {
-            if (kQ)
-              mma_from_tmem<W / 16>(tmem + kColX + 64u * m, st + W * m, b1_mn + where(i) + m * kMap,
-                                    id_x, acc);
-            else if (m == 0)
-              mma_from_tmem<W / 16>(tmem + kColX, st, b2_mn + where(i), id_x, acc);
-            mma_from_tmem<W / 16>(tmem + kColY + 64u * m, st + kDP + 8u * m,
-                                  b1_mn + where(i) + m * kMap, id_y, acc);
+            for (int m = 0; m < NM; ++m)
+              mma_scores<D / 16 / NM>(st + W * m, a1, kTile, b1 + where(i), kBlk, id_s,
+                                      m * (D / 16 / NM));
           }
-          // A commit stands between the products that read P and dS from TMEM and the
-          // scores that overwrite them in another MMA shape: only MMAs of one shape and
-          // accumulator are ordered by themselves.
-          mma_commit((i + 1) % kHalves == 0 ? &br.empty[(i / kHalves) % kSlots] : &br.order);
-          if (more) issue(i + 2);
-          const int jn = (i + 3) / kHalves;
-          ready = mbar_peek(&br.out_full[(i + 1) & 1], ((i + 1) >> 1) & 1) &&
-                  (i + 3 >= n || mbar_peek(&br.full[jn % kSlots], (jn / kSlots) & 1));
+          __syncwarp();
+          ok = __all_sync(0xFFFFFFFFu, i < 2 || mbar_wait(&br.y_done[i & 1], before, abort));
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (one) {
+            mma_scores<D / 16>(st + kDP, a2, kTile, b2 + where(i), kBlk, id_s, 0);
+            mma_commit(&br.s_full[i & 1]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
-      if (ok) {
-        if (one) mma_commit(&br.acc_full);
       } else {
+        const uint64_t b1_mn = sw128_desc(smem_u32(&sm.sa[0][0][0]), kBlk, 1024);
+        const uint64_t b2_mn = sw128_desc(smem_u32(&sm.sb[0][0][0]), kBlk, 1024);
+        for (int i = 0; ok && i < n; ++i) {  // X and Y of step i
+          ok = block_here(i) && mbar_wait(&br.out_full[i & 1], (i >> 1) & 1, abort);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (one) {
+            const uint32_t st = tmem + kStage0 + kStage * uint32_t(i & 1);
+            const uint32_t acc = i > 0 ? 1u : 0u;
+#pragma unroll
+            for (int m = 0; m < (kQ ? NM : 1); ++m) {
+              if (kQ)
+                mma_from_tmem<W / 16>(tmem + kColX + 64u * m, st + W * m,
+                                      b1_mn + where(i) + m * kMap, id_x, acc);
+              else
+                mma_from_tmem<W / 16>(tmem + kColX, st, b2_mn + where(i), id_x, acc);
+            }
+            mma_commit(&br.x_done[i & 1]);
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+              mma_from_tmem<W / 16>(tmem + kColY + 64u * m, st + kDP + 8u * m,
+                                    b1_mn + where(i) + m * kMap, id_y, acc);
+            mma_commit(&br.y_done[i & 1]);
+            if ((i + 1) % kHalves == 0) mma_commit(&br.empty[(i / kHalves) % kSlots]);
+          }
+          __syncwarp();
+        }
+        if (ok && one) mma_commit(&br.acc_full);
+      }
+      if (!ok) {
         fail_s(a.status, &br.abort, kDevErrTimeoutMma);
-        if (one) mma_commit(&br.drain);  // wait (bounded) for the MMAs issued before exit
+        if (one) mma_commit(&br.drain[warp >> 1]);  // wait (bounded) for the MMAs issued before exit
         int never = 0;
-        mbar_wait(&br.drain, 0, &never);
+        mbar_wait(&br.drain[warp >> 1], 0, &never);
       }
     }
   } else if (warp >= 4) {

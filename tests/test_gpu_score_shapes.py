@@ -65,3 +65,29 @@ def test_chains_of_unequal_length(d):
     p.check_ok()
     check_bias(p, out, lse)
     check_diff(p, out_d, None, None)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_same_bits_of_long_lists(d):
+    """Steps whose scores overwrite what the products of two steps before read: lists of
+    about 100 steps, more tiles than SMs, 10 runs of everything."""
+    desc = api.make_desc(1, 6, 8, 32, 32, d, 0.0)
+    gen = torch.Generator("cuda").manual_seed(d)
+    q, k, v, g = (torch.randn(1, 6, 8192, d, generator=gen, device="cuda").bfloat16() for _ in range(4))
+    ws = api.alloc_workspace(desc)
+    api.plan_mask(desc, torch.rand(6, 128, 128, generator=gen, device="cuda") < 0.6, ws)
+    bucket, n = api.relative_buckets(8, 32, 32)
+    table = torch.randn(6, n, generator=gen, device="cuda").bfloat16()
+    lam = torch.rand(6, generator=gen, device="cuda").bfloat16()
+    lse, lse2, out2 = torch.empty(1, 6, 8192, device="cuda"), torch.empty(2, 1, 6, 8192, device="cuda"), \
+        torch.empty_like(q)
+
+    def run():
+        a = api.fwd_bias(desc, q, k, v, table, bucket, ws, lse=lse)
+        b = api.fwd_diff(desc, q, k, v, lam, ws, out2=out2, lse=lse2)
+        return (a, b, out2.clone()) + api.bwd_bias(desc, q, k, v, table, bucket, a, g, lse, ws) + \
+            api.bwd_diff(desc, q, k, v, lam, b, out2, g, lse2, ws)
+    first = run()
+    for _ in range(10):
+        assert all(torch.equal(x, y) for x, y in zip(first, run()))
+    assert api.check(desc, ws) == api.SA_OK
