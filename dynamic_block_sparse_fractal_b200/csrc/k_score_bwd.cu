@@ -365,9 +365,9 @@ SA_HD int hist_floats(const Geometry& g) {
 // with the offset tables and the 16 histograms of the largest grid (pt + ph + pw
 // <= 66), a CTA's 227 KB
 static_assert(sizeof(SbSmem<128, 3>) + 1024 + sizeof(float) * (2 * kRelBiasMaxAxes - 3) +
-                      16 * sizeof(float) * (kRelBiasMaxAxes + 63) <= 232448,
+                      16 * sizeof(float) * (kRelBiasMaxAxes + 63) <= kSmemLimit,
               "shared memory of the key pass");
-static_assert(sizeof(SbSmem<128, 4>) + 1024 + sizeof(float) * (2 * kRelBiasMaxAxes - 3) <= 232448,
+static_assert(sizeof(SbSmem<128, 4>) + 1024 + sizeof(float) * (2 * kRelBiasMaxAxes - 3) <= kSmemLimit,
               "shared memory of the query pass");
 
 }  // namespace
@@ -1052,8 +1052,9 @@ static cudaError_t launch_pass(const ScoreBwdArgs& a, const Geometry& g, cudaStr
           : sizeof(float) * (relbias_offsets(g) + (kTable ? kSbRowWarps * hist_floats(g) : 0));
   const size_t need = sizeof(SbSmem<D, kTable ? 3 : kSbSlots>) + 1024 + tables;
   const int smem = int(need > 120 * 1024 ? need : 120 * 1024);
+  // (the limit belongs to the process: the same for every grid, as in the forward)
   cudaError_t e = cudaFuncSetAttribute(score_bwd_kernel<D, M, L, kQ>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
   return launch_early(score_bwd_kernel<D, M, L, kQ>, unsigned(g.ntile) * unsigned(g.BH),
                       kSbThreads, smem, stream, a, g);

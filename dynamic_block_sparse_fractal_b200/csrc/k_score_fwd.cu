@@ -61,7 +61,7 @@ struct __align__(1024) ScoreFwdSmem {
   int abort;
 };
 static_assert(sizeof(ScoreFwdSmem<128>) + 1024 + sizeof(float) * (2 * kRelBiasMaxAxes - 3) <=
-                  232448,
+                  kSmemLimit,
               "shared memory of the forward");
 
 // Slot of ring position k: the differential chains share a ring of all slots, the
@@ -524,8 +524,10 @@ static cudaError_t launch_score_fwd_m(const ScoreFwdArgs& a, const Geometry& g,
   size_t need = sizeof(ScoreFwdSmem<D>) + 1024;
   if (M != AttnMode::kDiff) need += relbias_offsets(g) * sizeof(float);
   const int smem = int(need > 120 * 1024 ? need : 120 * 1024);
+  // The limit belongs to the process, so it is the same for every grid: another
+  // thread's call of a smaller one may stand between these two lines.
   cudaError_t e = cudaFuncSetAttribute(score_fwd_kernel<D, M, L>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
   const bool one_tile = M == AttnMode::kDiff || a.split;
   const dim3 grid(unsigned(one_tile ? g.ntile : (g.ntile + 1) / 2), unsigned(g.BH));

@@ -178,6 +178,9 @@ inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned thread
   return cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 
+// Dynamic shared memory a CTA of sm_100a can have.
+constexpr int kSmemLimit = 227 * 1024;
+
 // Score functions besides q.k alone: a relative position bias, or the two maps of
 // differential attention.
 enum class AttnMode { kBias, kDiff };

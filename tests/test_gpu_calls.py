@@ -1,5 +1,6 @@
 """Calls beside other calls: after one that failed, from two threads at once."""
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -34,3 +35,52 @@ def test_a_failed_launch_is_not_reported_again():
         cu.cuStreamDestroy_v2(stream)
     side.synchronize()
     assert torch.equal(out, want)
+
+
+def test_two_threads_with_grids_of_different_size():
+    """The kernels' shared memory grows with the grid's offset tables: calls of a large and
+    a small grid from two threads at once, each on a stream of its own."""
+    jobs = []
+    for i, grid in enumerate(((400, 8, 8), (2, 8, 8))):
+        for d in (64, 128):
+            desc = api.make_desc(1, 1, *grid, d, 0.0)
+            S = grid[0] * 64
+            gen = torch.Generator("cuda").manual_seed(i)
+            x = [torch.randn(1, 1, S, d, generator=gen, device="cuda").bfloat16() for _ in range(4)]
+            ws = api.alloc_workspace(desc)
+            api.plan_mask(desc, torch.eye(grid[0], dtype=torch.bool, device="cuda"), ws)
+            bucket, n = api.relative_buckets(*grid)
+            table = torch.randn(1, n, generator=gen, device="cuda").bfloat16()
+            jobs.append((desc, x, ws, table, bucket))
+
+    def step(job, stream):
+        desc, (q, k, v, g), ws, table, bucket = job
+        lse = torch.empty(q.shape[:3], device="cuda")
+        out = api.fwd_bias(desc, q, k, v, table, bucket, ws, lse=lse, stream=stream)
+        return (out, lse) + api.bwd_bias(desc, q, k, v, table, bucket, out, g, lse, ws, stream=stream)
+
+    want = [step(job, None) for job in jobs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(mine):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(200):
+                for i in mine:
+                    try:
+                        got = step(jobs[i], stream)
+                    except api.SparseAttnError as e:
+                        wrong.append(str(e))
+                        return
+            stream.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[mine[-1]])):
+                wrong.append(f"outputs of job {mine[-1]}")
+
+    threads = [threading.Thread(target=work, args=(m,)) for m in ((0, 1), (2, 3), (1, 0), (3, 2))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    assert all(api.check(desc, ws) == api.SA_OK for desc, _, ws, _, _ in jobs)
