@@ -65,6 +65,7 @@ __device__ __forceinline__ RelBiasRow relbias_row(const Geometry& g, int blk, in
 // into the block is at t + sign dt, h + sign dh, w + sign dw.
 __device__ __forceinline__ void relbias_block(const Geometry& g, const RelBiasRow& r, int kb,
                                               int sign, int& t, int& h, int& w) {
+  kb = kb < g.nb ? kb : 0;  // as the loader reads, and reports, a list entry out of range
   const int tb = div_by(kb, r.mf);
   const int rest = kb - tb * (g.nh * g.nw);
   const int hb = div_by(rest, r.mw);

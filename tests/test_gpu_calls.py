@@ -84,3 +84,30 @@ def test_two_threads_with_grids_of_different_size():
         t.join()
     assert not wrong, wrong
     assert all(api.check(desc, ws) == api.SA_OK for desc, _, ws, _, _ in jobs)
+
+
+@pytest.mark.parametrize("tile,d", [(None, 128), (None, 64), ((1, 2, 32), 64)])
+def test_a_list_entry_out_of_range_is_reported_and_read_as_block_0(tile, d):
+    """A plan's list with a block id that the grid does not have: the status says so, and
+    the bias of that entry is block 0's, as its keys and values are."""
+    desc = api.make_desc(1, 2, 2, 8, 64, d, 0.0, tile=tile)
+    gen = torch.Generator("cuda").manual_seed(3)
+    q, k, v, g = (torch.randn(1, 2, 1024, d, generator=gen, device="cuda").bfloat16() for _ in range(4))
+    bucket, n = api.relative_buckets(2, 8, 64)
+    table = torch.randn(2, n, generator=gen, device="cuda").bfloat16()
+    res = []
+    for first in (0, 3):
+        mask = torch.zeros(16, 16, dtype=torch.bool, device="cuda")
+        mask[:, [first, 6]] = True
+        ws = api.alloc_workspace(desc)
+        api.plan_mask(desc, mask, ws)
+        if first:
+            entries = api.get_mask(desc, ws)["tile_idx"][:, :, 0]
+            assert bool((entries & 0xFFFF == first).all())
+            entries |= 0xFFFF
+        lse = torch.empty(q.shape[:3], device="cuda")
+        out = api.fwd_bias(desc, q, k, v, table, bucket, ws, lse=lse)
+        dq = api.bwd_bias(desc, q, k, v, table, bucket, out, g, lse, ws)[0]
+        res.append((out, lse, dq))
+        assert api.check(desc, ws) == (api.SA_ERR_DEVICE_TIMEOUT if first else api.SA_OK)
+    assert all(torch.equal(a, b) for a, b in zip(*res))
