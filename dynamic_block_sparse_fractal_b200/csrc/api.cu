@@ -654,7 +654,8 @@ const char* sparse_attn_status_string(sa_status status) {
     case SA_ERR_UNSUPPORTED: return "unsupported configuration";
     case SA_ERR_WORKSPACE: return "workspace too small";
     case SA_ERR_CUDA: return "CUDA runtime error";
-    case SA_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait ran out (device status set)";
+    case SA_ERR_DEVICE_TIMEOUT:
+      return "a kernel's bounded wait ran out or it met an index out of range (device status set)";
   }
   return "unknown status";
 }

@@ -33,7 +33,7 @@
  *     S = T*Hh*Ww tokens ordered (t, h, w), t outermost, d innermost,
  *     contiguous, bf16 (raw 16-bit storage), 16-byte aligned.
  *   - Device-side failures (a bounded wait that ran out, an out-of-range block
- *     index) are recorded in a status word inside the workspace and reported
+ *     or bucket index) are recorded in a status word inside the workspace and reported
  *     by sparse_attn_check. No kernel of this library traps.
  */
 #ifndef SPARSE_ATTN_H
@@ -89,7 +89,9 @@ typedef enum sa_status {
   SA_ERR_WORKSPACE = 3,       /* workspace smaller than
                                  sparse_attn_workspace_size() */
   SA_ERR_CUDA = 4,            /* a CUDA runtime call or launch failed */
-  SA_ERR_DEVICE_TIMEOUT = 5   /* a kernel's bounded wait ran out */
+  SA_ERR_DEVICE_TIMEOUT = 5   /* a kernel's bounded wait ran out, or it met an
+                                 index out of range (a block id of a list, an
+                                 entry of a bucket map) and read entry 0 */
 } sa_status;
 
 /* Bytes of device workspace a plan for `desc` needs (written to *bytes). */
