@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
       for (int j = 0; ok && j < n; ++j) {
         const bool has_s = j + 2 < n;
         const int sv = ring_slot<kDiff>(x, k), sk = ring_slot<kDiff>(x, k + 1);
-        ok = mbar_wait(&sm.p_full[x][j & 1], (j >> 1) & 1, abort) &&
-             mbar_wait(&sm.full[sv], (k / kRing) & 1, abort);
+        ok = mbar_wait(&sm.full[sv], (k / kRing) & 1, abort) &&
+             mbar_wait(&sm.p_full[x][j & 1], (j >> 1) & 1, abort);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc_fence_after_sync();
