@@ -26,7 +26,7 @@
 // - R P K. That takes out D~'s error and the part of the roundings that lies along
 // the row's mean key, which is the largest where keys share a component. (2-norm
 // error of dQ against 64 bits, bf16 outputs: 4.5e-3 with D~ alone, 2.9e-3 with D,
-// 2.3e-3 with R; the bf16 rounding of dQ itself is 1.7e-3. Gradients of the table
+// 2.2e-3 with R; the bf16 rounding of dQ itself is 1.7e-3. Gradients of the table
 // and of lambda: up to 7e-3 with D~, 2e-3 with D.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

